@@ -79,7 +79,8 @@ typedef enum {
   QMM_ERR_ALIGNMENT = 4,     /* null or under-aligned pointer */
   QMM_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed */
   QMM_ERR_TIMEOUT = 6,       /* a bounded device-side wait gave up */
-  QMM_ERR_BAD_EXPERT_ID = 7  /* (device) an id outside [0, num_experts) */
+  QMM_ERR_BAD_EXPERT_ID = 7, /* (device) an id outside [0, num_experts) */
+  QMM_ERR_BAD_TOKEN_ID = 8   /* (device) a token id outside [0, rows) */
 } qmm_status;
 
 /* QMM_U8 is only the storage of the microscaled modes' scale bytes. */
@@ -391,6 +392,107 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
                                    int64_t batch, int64_t top_k, int64_t ne11,
                                    const qmm_expert_stack* w, void* out, qmm_dtype out_dtype,
                                    int32_t* d_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Fine-tuning and serving a packed model: the lookup in a packed table, the
+ * dense gated feed-forward projection, and the gradients of both and of
+ * qmm_matmul.  The codes are constants; the trainable parameters of a packed
+ * weight w_hat = q * scale + bias are its scales and biases:
+ *   dscales[n, j] = sum over k in group j of dW[n, k] * q[n, k],
+ *   dbiases[n, j] = sum over k in group j of dW[n, k],
+ * dW the gradient of the dense matrix, which is never stored.
+ *
+ * The gated block and the matmul gradients take bf16 or f16 activations of
+ * the scales' dtype, affine weights and the [N, K] layout (transpose = 1); f32
+ * activations and the microscaled modes return QMM_ERR_UNSUPPORTED.  Their
+ * products run on the tensor cores with fp32 accumulation.  For more than 16
+ * tokens the operands are the activations' 16-bit type: each dequantized
+ * weight is rounded once to it (as in qmm_matmul), and so are dg and du of
+ * the gated block's gradient.  An f32 output is the same arithmetic without
+ * the last rounding.  Results do not depend on timing: the same call gives
+ * the same bits.
+ *
+ * Workspaces are device memory of the caller, 16-byte aligned, of at least
+ * the bytes that the matching ..._workspace_bytes call gives; a call writes
+ * what it reads there, so the contents need no preparation.  Two calls that
+ * may overlap on the GPU (two streams, two captured graphs) need two.
+ * ------------------------------------------------------------------------ */
+
+/* Lookup: out[t, :] = alpha * w_hat[ids[t], :] (the row as qmm_dequantize
+ * gives it in fp32, one fp32 product with alpha, one rounding to out_dtype).
+ * ids: device int32[n]; out: [n, w->cols] in out_dtype (any float type).  All
+ * modes.  A token whose id is outside [0, w->rows) gets a zero row and sets
+ * QMM_ERR_BAD_TOKEN_ID in *d_status (may be NULL).  n == 0 is a no-op.
+ * Errors: qmm_dequantize's for w; DTYPE (out_dtype), INVALID_ARG (n outside
+ * [0, 2^31 - 1]), ALIGNMENT (ids and d_status 4-byte, out 16-byte),
+ * UNSUPPORTED (device), CUDA. */
+qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha, void* out,
+                         qmm_dtype out_dtype, int32_t* d_status, void* stream);
+
+/* Workspace bytes of qmm_embedding_backward (-1 when n or rows is outside
+ * [0, 2^31 - 1] or cols <= 0). */
+int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
+
+/* Gradient of the lookup in the table's scales and biases, with
+ * dW[r, :] = alpha * sum of dy[t, :] over the tokens t with ids[t] = r, taken
+ * in token order in fp32.  dy: [n, w->cols] in any float type; dscales,
+ * dbiases: [w->rows, w->cols / group_size] in g_dtype (any float type), written
+ * whole: rows that no token names get zeros, for n == 0 all of them.  Affine
+ * tables; the scales and biases themselves are not read.  A token whose id is
+ * outside [0, w->rows) adds nothing and sets QMM_ERR_BAD_TOKEN_ID in *d_status
+ * (may be NULL).
+ * Errors: qmm_dequantize's for w; UNSUPPORTED (microscaled, device), DTYPE,
+ * INVALID_ARG (n, workspace_bytes), ALIGNMENT (dy, dscales, dbiases, workspace
+ * 16-byte, ids and d_status 4-byte), CUDA. */
+qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int32_t* ids, int64_t n,
+                                  const qmm_qweight* w, float alpha, void* dscales, void* dbiases,
+                                  qmm_dtype g_dtype, void* workspace, int64_t workspace_bytes, int32_t* d_status,
+                                  void* stream);
+
+/* The gated projection: h[M, F] = SiLU(x . dequant(gate)^T) * (x .
+ * dequant(up)^T), SiLU(g) = g / (1 + exp(-g)): the dense form of
+ * qmm_moe_gemv_id_gate_up_silu, for any number of tokens.  gate and up: [F, K]
+ * with the same parameters.  h_dtype is x_dtype or QMM_F32.  g_pre and u_pre
+ * (both NULL, or both [M, F] in x_dtype) receive the two projections, which
+ * the backward pass reads.  M == 0 or F == 0 is a no-op.
+ * Errors: INVALID_ARG (shape rules, K, gate and up differ, one of g_pre and
+ * u_pre missing), UNSUPPORTED (see above, sizes past 2^31 - 1, device), DTYPE,
+ * ALIGNMENT (x, h, g_pre, u_pre 16-byte), CUDA. */
+qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
+                            const qmm_qweight* up, void* h, qmm_dtype h_dtype, void* g_pre, void* u_pre,
+                            void* stream);
+
+/* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1]). */
+int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/* Gradients of y = x . dequant(W)^T (qmm_matmul, transpose = 1): dx[M, K] = dy .
+ * dequant(W) in x_dtype, and dscales, dbiases [N, K / group_size] in g_dtype
+ * (x_dtype or QMM_F32) with dW = dy^T x.  dy: [M, N], x: [M, K] in x_dtype.  dx
+ * may be NULL, or both dscales and dbiases (x is then not read).  M == 0
+ * writes zero parameter gradients, N == 0 a zero dx.
+ * Errors: INVALID_ARG (shape rules, K, nothing to compute, workspace_bytes),
+ * UNSUPPORTED, DTYPE, ALIGNMENT (16-byte), CUDA. */
+qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype, int64_t M, int64_t K,
+                               const qmm_qweight* w, void* dx, void* dscales, void* dbiases, qmm_dtype g_dtype,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of qmm_gate_up_silu_backward (-1 for a size outside
+ * [0, 2^31 - 1]). */
+int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F);
+
+/* Gradients of the gated projection from its saved g_pre and u_pre: with
+ * p = 1 / (1 + exp(-g)), du = dh * g * p and dg = dh * u * p * (1 + g * (1 - p)),
+ *   dx = dg . dequant(gate) + du . dequant(up)  in x_dtype,
+ *   dgate_scales, dgate_biases from dW = dg^T x, dup_scales, dup_biases from
+ *   dW = du^T x, [F, K / group_size] each in g_dtype (x_dtype or QMM_F32).
+ * dh, g_pre, u_pre: [M, F] in x_dtype.  dx may be NULL, or all four parameter
+ * gradients.  M == 0 writes zero parameter gradients, F == 0 a zero dx.
+ * Errors: as qmm_matmul_backward and qmm_gate_up_silu. */
+qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* g_pre, const void* u_pre,
+                                     qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
+                                     const qmm_qweight* up, void* dx, void* dgate_scales, void* dgate_biases,
+                                     void* dup_scales, void* dup_biases, qmm_dtype g_dtype, void* workspace,
+                                     int64_t workspace_bytes, void* stream);
 
 /* Diagnostic of the bounded device-side waits (not a step of the method).
  * Every TMA-fed kernel here waits on shared-memory mbarriers with a poll

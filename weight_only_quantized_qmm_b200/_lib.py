@@ -20,6 +20,7 @@ QMM_ERR_ALIGNMENT = 4
 QMM_ERR_CUDA = 5
 QMM_ERR_TIMEOUT = 6
 QMM_ERR_BAD_EXPERT_ID = 7
+QMM_ERR_BAD_TOKEN_ID = 8
 
 QMM_F32, QMM_F16, QMM_BF16, QMM_U8 = 0, 1, 2, 3
 QMM_MODE_AFFINE, QMM_MODE_MXFP4, QMM_MODE_MXFP8, QMM_MODE_NVFP4 = 0, 1, 2, 3
@@ -33,6 +34,9 @@ EXPORTS = (
     "qmm_moe_compute_ids_tpe", "qmm_moe_gemm_id", "qmm_moe_gemm_id_noalloc",
     "qmm_selftest_bounded_wait", "qmm_matmul_parts", "qmm_quantize_dynamic_int8",
     "qmm_dequantize_dynamic_int8", "qmm_matmul_dynamic_int8", "qmm_moe_gemm_workspace_bytes_gathered",
+    "qmm_embedding", "qmm_embedding_backward_workspace_bytes", "qmm_embedding_backward",
+    "qmm_gate_up_silu", "qmm_matmul_backward_workspace_bytes", "qmm_matmul_backward",
+    "qmm_gate_up_silu_backward_workspace_bytes", "qmm_gate_up_silu_backward",
 )
 
 
@@ -112,6 +116,23 @@ def load() -> ctypes.CDLL:
     L.qmm_dequantize_dynamic_int8.restype = c_int
     L.qmm_matmul_dynamic_int8.argtypes = [vp, c_int, i64, i64, vp, i64, vp, vp, c_int, vp]
     L.qmm_matmul_dynamic_int8.restype = c_int
+    L.qmm_embedding.argtypes = [vp, i64, qwp, ctypes.c_float, vp, c_int, vp, vp]
+    L.qmm_embedding.restype = c_int
+    L.qmm_embedding_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qmm_embedding_backward_workspace_bytes.restype = i64
+    L.qmm_embedding_backward.argtypes = [vp, c_int, vp, i64, qwp, ctypes.c_float, vp, vp, c_int, vp, i64, vp, vp]
+    L.qmm_embedding_backward.restype = c_int
+    L.qmm_gate_up_silu.argtypes = [vp, c_int, i64, i64, qwp, qwp, vp, c_int, vp, vp, vp]
+    L.qmm_gate_up_silu.restype = c_int
+    L.qmm_matmul_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qmm_matmul_backward_workspace_bytes.restype = i64
+    L.qmm_matmul_backward.argtypes = [vp, vp, c_int, i64, i64, qwp, vp, vp, vp, c_int, vp, i64, vp]
+    L.qmm_matmul_backward.restype = c_int
+    L.qmm_gate_up_silu_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qmm_gate_up_silu_backward_workspace_bytes.restype = i64
+    L.qmm_gate_up_silu_backward.argtypes = [vp, vp, vp, vp, c_int, i64, i64, qwp, qwp, vp, vp, vp, vp, vp, c_int, vp,
+                                            i64, vp]
+    L.qmm_gate_up_silu_backward.restype = c_int
     _lib = L
     return L
 

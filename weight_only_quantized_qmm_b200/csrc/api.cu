@@ -50,7 +50,6 @@ static bool gs_ok(int g) { return g == 32 || g == 64 || g == 128; }
 static bool packable(int64_t cols, int gs, int bits) {
   return bits_ok(bits) && gs_ok(gs) && cols > 0 && cols % gs == 0 && (cols * bits) % 32 == 0;
 }
-static bool aligned4(const void* p) { return p && ((reinterpret_cast<uintptr_t>(p) & 3u) == 0); }
 
 // Largest MoE call the kernels' per-CTA plans are sized for (pairs, experts).
 constexpr int64_t kMaxMoePairs = 65536;
@@ -73,7 +72,7 @@ static bool mx_params(int mode, int* bits, int* gs) {
   }
 }
 
-static qmm_status check_qweight(const qmm_qweight* w) {
+qmm_status check_qweight(const qmm_qweight* w) {
   if (!w) return QMM_ERR_INVALID_ARG;
   if (w->mode != QMM_MODE_AFFINE) {
     int bits = 0, gs = 0;
@@ -139,6 +138,7 @@ const char* qmm_status_string(int s) {
     case QMM_ERR_CUDA: return "CUDA runtime error";
     case QMM_ERR_TIMEOUT: return "device-side wait timed out";
     case QMM_ERR_BAD_EXPERT_ID: return "expert id out of range";
+    case QMM_ERR_BAD_TOKEN_ID: return "token id out of range";
     default: return "unknown status";
   }
 }

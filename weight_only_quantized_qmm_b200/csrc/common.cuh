@@ -70,6 +70,8 @@ namespace qmm_host {
 inline int dtype_size(qmm_dtype d) { return d == QMM_F32 ? 4 : 2; }
 inline bool dtype_ok(int d) { return d == QMM_F32 || d == QMM_F16 || d == QMM_BF16; }
 inline bool aligned16(const void* p) { return p && ((reinterpret_cast<uintptr_t>(p) & 15u) == 0); }
+inline bool aligned4(const void* p) { return p && ((reinterpret_cast<uintptr_t>(p) & 3u) == 0); }
+qmm_status check_qweight(const qmm_qweight* w);  // shape, mode, dtype and alignment rules (api.cu)
 int num_sms();
 qmm_status launch_status(cudaError_t e);
 }  // namespace qmm_host
