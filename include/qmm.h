@@ -462,7 +462,8 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
                             const qmm_qweight* up, void* h, qmm_dtype h_dtype, void* g_pre, void* u_pre,
                             void* stream);
 
-/* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1]). */
+/* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1]
+ * or M * N past 2^59). */
 int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
 /* Gradients of y = x . dequant(W)^T (qmm_matmul, transpose = 1): dx[M, K] = dy .
@@ -477,7 +478,7 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of qmm_gate_up_silu_backward (-1 for a size outside
- * [0, 2^31 - 1]). */
+ * [0, 2^31 - 1] or M * F past 2^59). */
 int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F);
 
 /* Gradients of the gated projection from its saved g_pre and u_pre: with

@@ -6,181 +6,146 @@
 //   dW = dy^T x;  dscales[n, j] = sum over k in group j of dW[n, k] q[n, k],
 //   dbiases[n, j] = sum over k in group j of dW[n, k]
 // (w_hat = q * scale + bias; the codes are constants, dW is never stored).
+//
+// For more than 16 tokens, and for every gradient, the products run on the
+// tensor cores (pair_gemm.cuh).  The gated block's gradient is three launches:
+// dg and du into the workspace, the dx product over gate and up together, and
+// the parameter gradients of both.
 #include <algorithm>
 
-#include "common.cuh"
+#include "pair_gemm.cuh"
 
 namespace qmm {
+namespace pg {
+cudaError_t dispatch_b2(int, bool, const Args&, const CUtensorMap (&)[3], int, cudaStream_t);
+cudaError_t dispatch_b3(int, bool, const Args&, const CUtensorMap (&)[3], int, cudaStream_t);
+cudaError_t dispatch_b4(int, bool, const Args&, const CUtensorMap (&)[3], int, cudaStream_t);
+cudaError_t dispatch_b6(int, bool, const Args&, const CUtensorMap (&)[3], int, cudaStream_t);
+cudaError_t dispatch_b8(int, bool, const Args&, const CUtensorMap (&)[3], int, cudaStream_t);
+}  // namespace pg
+
 namespace ffn {
 
-constexpr int kT = 16;  // tile of the simple kernels
-
-template <int B>
-__device__ __forceinline__ float code_at(const uint32_t* row, int64_t i) {
-  const int64_t bit = i * B;
-  const int sh = (int)(bit & 31);
-  uint32_t v = row[bit >> 5] >> sh;
-  if (sh + B > 32) v |= row[(bit >> 5) + 1] << (32 - sh);
-  return (float)(v & ((1u << B) - 1u));
-}
-
-struct Weight {
-  const uint32_t* packed;
-  const void* scales;
-  const void* biases;
-};
-
-template <int B, typename T>
-__device__ __forceinline__ float w_at(const Weight& w, int64_t n, int64_t k, int64_t K, int gs) {
-  const int64_t G = K / gs;
-  return fmaf(code_at<B>(w.packed + n * (K * B / 32), k), to_f32(reinterpret_cast<const T*>(w.scales)[n * G + k / gs]),
-              to_f32(reinterpret_cast<const T*>(w.biases)[n * G + k / gs]));
-}
-
-template <int B, typename T>
-__global__ void __launch_bounds__(kT * kT)
-gate_up_kernel(const T* __restrict__ x, int M, int K, int F, int gs, Weight gate, Weight up, void* h, int h_dtype, T* gp,
-               T* upre) {
-  __shared__ float xs[kT][kT + 1], ws[2][kT][kT + 1];
-  const int tx = threadIdx.x % kT, ty = threadIdx.x / kT;
-  const int64_t m = (int64_t)blockIdx.y * kT + ty, n = (int64_t)blockIdx.x * kT + tx;
-  float g = 0.0f, u = 0.0f;
-  for (int k0 = 0; k0 < K; k0 += kT) {
-    const int64_t wr = (int64_t)blockIdx.x * kT + ty;
-    xs[ty][tx] = m < M ? to_f32(x[m * K + k0 + tx]) : 0.0f;
-    ws[0][ty][tx] = wr < F ? w_at<B, T>(gate, wr, k0 + tx, K, gs) : 0.0f;
-    ws[1][ty][tx] = wr < F ? w_at<B, T>(up, wr, k0 + tx, K, gs) : 0.0f;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kT; ++k) {
-      g = fmaf(xs[ty][k], ws[0][tx][k], g);
-      u = fmaf(xs[ty][k], ws[1][tx][k], u);
-    }
-    __syncthreads();
-  }
-  if (m < M && n < F) {
-    store_as(h, h_dtype, m * F + n, g / (1.0f + expf(-g)) * u);
-    if (gp) {
-      gp[m * F + n] = from_f32<T>(g);
-      upre[m * F + n] = from_f32<T>(u);
-    }
-  }
-}
-
-// dg, du of one element
-__device__ __forceinline__ void silu_mul_grad(float dh, float g, float u, float& dg, float& du) {
-  const float p = 1.0f / (1.0f + expf(-g));
-  du = dh * (g * p);
-  dg = dh * u * (p * (1.0f + g * (1.0f - p)));
-}
-
+// dg and du, rounded once to T (they are operands of 16-bit products), in rows
+// of ld elements
 template <typename T>
 __global__ void __launch_bounds__(256)
-act_grad_kernel(const T* __restrict__ dh, const T* __restrict__ g, const T* __restrict__ u, int64_t n, T* dg, T* du) {
+act_grad_kernel(const T* __restrict__ dh, const T* __restrict__ g, const T* __restrict__ u, int64_t n, int F, int ld,
+                T* __restrict__ dg, T* __restrict__ du) {
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    float a, b;
-    silu_mul_grad(to_f32(dh[i]), to_f32(g[i]), to_f32(u[i]), a, b);
-    dg[i] = from_f32<T>(a);
-    du[i] = from_f32<T>(b);
+    const int64_t at = i / F * ld + i % F;
+    const float a = to_f32(dh[i]), b = to_f32(g[i]), c = to_f32(u[i]);
+    const float p = 1.0f / (1.0f + expf(-b));
+    dg[at] = from_f32<T>(a * c * (p * (1.0f + b * (1.0f - p))));
+    du[at] = from_f32<T>(a * (b * p));
   }
 }
 
-template <int B, typename T>
-__global__ void __launch_bounds__(kT * kT)
-dx_kernel(const T* __restrict__ dy0, const T* __restrict__ dy1, int M, int K, int N, int gs, Weight w0, Weight w1,
-          int parts, T* dx) {
-  __shared__ float ys[kT][kT + 1], ws[kT][kT + 1];
-  const int tx = threadIdx.x % kT, ty = threadIdx.x / kT;
-  const int64_t m = (int64_t)blockIdx.y * kT + ty, k = (int64_t)blockIdx.x * kT + tx;
-  float acc = 0.0f;
-  for (int part = 0; part < parts; ++part)
-    for (int n0 = 0; n0 < N; n0 += kT) {
-      ys[ty][tx] = m < M && n0 + tx < N ? to_f32((part ? dy1 : dy0)[m * N + n0 + tx]) : 0.0f;
-      ws[ty][tx] = n0 + ty < N && k < K ? w_at<B, T>(part ? w1 : w0, n0 + ty, k, K, gs) : 0.0f;
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < kT; ++n) acc = fmaf(ys[ty][n], ws[n][tx], acc);
-      __syncthreads();
-    }
-  if (m < M && k < K) dx[m * K + k] = from_f32<T>(acc);
-}
-
-// one warp per (row, group)
-template <int B, typename T>
+// rows of n elements to rows of ld
 __global__ void __launch_bounds__(256)
-param_grad_kernel(const T* __restrict__ dy, const T* __restrict__ x, int M, int K, int N, int gs,
-                  const uint32_t* __restrict__ packed, void* dscales, void* dbiases, int g_dtype) {
-  const int64_t G = K / gs, id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (id >= (int64_t)N * G) return;
-  const int64_t n = id / G, j = id % G;
-  float ds = 0.0f, db = 0.0f;
-  for (int64_t k = j * gs + lane; k < (j + 1) * gs; k += 32) {
-    float a = 0.0f;
-    for (int64_t m = 0; m < M; ++m) a = fmaf(to_f32(dy[m * N + n]), to_f32(x[m * K + k]), a);
-    ds = fmaf(a, code_at<B>(packed + n * ((int64_t)K * B / 32), k), ds);
-    db += a;
+pad_kernel(const uint16_t* __restrict__ src, int64_t n, int F, int ld, uint16_t* __restrict__ dst) {
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    dst[i / F * ld + i % F] = src[i];
+}
+
+static int blocks_for(int64_t n) { return (int)std::min<int64_t>((n + 255) / 256, (int64_t)qmm_host::num_sms() * 8); }
+
+static pg::Weight weight_of(const qmm_qweight* w) { return pg::Weight{w->packed, w->scales, w->biases}; }
+
+static pg::Args args_of(int64_t M, int64_t K, const qmm_qweight* w0, const qmm_qweight* w1, int x_dtype) {
+  pg::Args p{};
+  p.M = (int)M;
+  p.K = (int)K;
+  p.N = (int)w0->rows;
+  p.parts = w1 ? 2 : 1;
+  p.w[0] = weight_of(w0);
+  p.w[1] = weight_of(w1 ? w1 : w0);
+  p.lgs = w0->group_size == 32 ? 5 : w0->group_size == 64 ? 6 : 7;
+  p.f16 = x_dtype == QMM_F16;
+  return p;
+}
+
+static cudaError_t run(int op, int bits, bool pair, pg::Args& p, const CUtensorMap (&tm)[3], cudaStream_t st) {
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * (op == pg::DP ? p.parts : 1);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  int clusters = (int)std::min<int64_t>(tiles, qmm_host::num_sms() / 2);
+  p.splits = 1;
+  if (!pair) {
+    // few tiles: CTAs share a tile by cutting its sum, at least 4 steps each
+    while (p.splits < 8 && tiles * p.splits * 2 <= qmm_host::num_sms() && p.steps >= 8 * p.splits) p.splits *= 2;
+    clusters = p.splits > 1 ? (int)tiles : (int)std::min<int64_t>(tiles, qmm_host::num_sms());
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    ds += __shfl_xor_sync(0xffffffffu, ds, o);
-    db += __shfl_xor_sync(0xffffffffu, db, o);
-  }
-  if (lane == 0) {
-    store_as(dscales, g_dtype, id, ds);
-    store_as(dbiases, g_dtype, id, db);
+  switch (bits) {
+    case 2: return pg::dispatch_b2(op, pair, p, tm, clusters, st);
+    case 3: return pg::dispatch_b3(op, pair, p, tm, clusters, st);
+    case 4: return pg::dispatch_b4(op, pair, p, tm, clusters, st);
+    case 6: return pg::dispatch_b6(op, pair, p, tm, clusters, st);
+    default: return pg::dispatch_b8(op, pair, p, tm, clusters, st);
   }
 }
 
-static Weight weight_of(const qmm_qweight* w) { return Weight{w->packed, w->scales, w->biases}; }
+static int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-#define QMM_BITS(bits, CALL) \
-  switch (bits) {            \
-    case 2: CALL(2); break;  \
-    case 3: CALL(3); break;  \
-    case 4: CALL(4); break;  \
-    case 6: CALL(6); break;  \
-    default: CALL(8); break; \
-  }
-
-template <typename T>
-static cudaError_t forward_t(const void* x, int64_t M, int64_t K, const qmm_qweight* gate, const qmm_qweight* up, void* h,
-                             int h_dtype, void* gp, void* upre, cudaStream_t st) {
-  const int64_t F = gate->rows;
-  const dim3 grid((unsigned)((F + kT - 1) / kT), (unsigned)((M + kT - 1) / kT));
-#define QMM_C(BB)                                                                                                    \
-  gate_up_kernel<BB, T><<<grid, kT * kT, 0, st>>>((const T*)x, (int)M, (int)K, (int)F, gate->group_size,             \
-                                                  weight_of(gate), weight_of(up), h, h_dtype, (T*)gp, (T*)upre)
-  QMM_BITS(gate->bits, QMM_C)
-#undef QMM_C
-  return cudaGetLastError();
+static cudaError_t forward(const void* x, int x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
+                           const qmm_qweight* up, void* h, int h_dtype, void* gp, void* upre, cudaStream_t st) {
+  pg::Args p = args_of(M, K, gate, up, x_dtype);
+  const bool pair = M > 128;
+  p.m_tiles = ceil_div(M, pair ? 256 : 128);
+  p.n_tiles = ceil_div(p.N, 128);
+  p.steps = ceil_div(K, pg::kBK);
+  p.out[0] = h;
+  p.out[1] = gp;
+  p.out[2] = upre;
+  p.out_dtype = h_dtype;
+  CUtensorMap tm[3];
+  if (!pg::make_map(&tm[0], x, p.f16, M, K, K, 128)) return cudaErrorInvalidValue;
+  tm[1] = tm[2] = tm[0];
+  return run(pg::FWD, gate->bits, pair, p, tm, st);
 }
 
-template <typename T>
-static cudaError_t backward_t(const void* dy0, const void* dy1, const void* x, int64_t M, int64_t K,
-                              const qmm_qweight* w0, const qmm_qweight* w1, void* dx, void* const* grads, int g_dtype,
-                              cudaStream_t st) {
+// dy0 (and dy1): [M, N] in rows of ld elements, ld a multiple of 8
+static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const void* x, int x_dtype, int64_t M,
+                            int64_t K, const qmm_qweight* w0, const qmm_qweight* w1, void* dx, void* const* grads,
+                            int g_dtype, cudaStream_t st) {
   const int64_t N = w0->rows;
-  if (dx && M > 0) {
-    const dim3 grid((unsigned)((K + kT - 1) / kT), (unsigned)((M + kT - 1) / kT));
-#define QMM_C(BB)                                                                                            \
-  dx_kernel<BB, T><<<grid, kT * kT, 0, st>>>((const T*)dy0, (const T*)dy1, (int)M, (int)K, (int)N, w0->group_size, \
-                                             weight_of(w0), weight_of(w1 ? w1 : w0), w1 ? 2 : 1, (T*)dx)
-    QMM_BITS(w0->bits, QMM_C)
-#undef QMM_C
+  if (M == 0 || N == 0) {  // empty sums
+    cudaError_t e = cudaSuccess;
+    if (dx && M > 0) e = cudaMemsetAsync(dx, 0, (size_t)(M * K * 2), st);
+    const size_t bytes = (size_t)(N * (K / w0->group_size) * qmm_host::dtype_size((qmm_dtype)g_dtype));
+    for (int i = 0; i < (w1 ? 4 : 2) && grads[0] && bytes && e == cudaSuccess; ++i) e = cudaMemsetAsync(grads[i], 0, bytes, st);
+    return e;
   }
-  for (int p = 0; grads[0] && p < (w1 ? 2 : 1); ++p) {
-    const int64_t items = N * (K / w0->group_size);
-    const unsigned grid = (unsigned)((items + 7) / 8);
-    if (items == 0) continue;
-#define QMM_C(BB)                                                                                                   \
-  param_grad_kernel<BB, T><<<grid, 256, 0, st>>>((const T*)(p ? dy1 : dy0), (const T*)x, (int)M, (int)K, (int)N,    \
-                                                 w0->group_size, p ? w1->packed : w0->packed, grads[2 * p],         \
-                                                 grads[2 * p + 1], g_dtype)
-    QMM_BITS(w0->bits, QMM_C)
-#undef QMM_C
+  CUtensorMap tm[3];
+  if (dx) {
+    pg::Args p = args_of(M, K, w0, w1, x_dtype);
+    const bool pair = M > 128;
+    p.m_tiles = ceil_div(M, pair ? 256 : 128);
+    p.n_tiles = ceil_div(K, 256);
+    p.steps = p.parts * ceil_div(N, pg::kBK);
+    p.out[0] = dx;
+    p.out_dtype = x_dtype;
+    if (!pg::make_map(&tm[0], dy0, p.f16, M, N, ld, 128) || !pg::make_map(&tm[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 128))
+      return cudaErrorInvalidValue;
+    tm[2] = tm[0];
+    const cudaError_t e = run(pg::DX, w0->bits, pair, p, tm, st);
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  if (grads[0]) {
+    pg::Args p = args_of(M, K, w0, w1, x_dtype);
+    p.m_tiles = ceil_div(N, 256);
+    p.n_tiles = ceil_div(K, 256);
+    p.steps = ceil_div(M, pg::kBK);
+    for (int i = 0; i < 4; ++i) p.out[i] = grads[i];
+    p.out_dtype = g_dtype;
+    if (!pg::make_map(&tm[0], dy0, p.f16, M, N, ld, 64) || !pg::make_map(&tm[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 64) ||
+        !pg::make_map(&tm[2], x, p.f16, M, K, K, 64))
+      return cudaErrorInvalidValue;
+    return run(pg::DP, w0->bits, true, p, tm, st);
+  }
+  return cudaSuccess;
 }
+
+static int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
 
 }  // namespace ffn
 }  // namespace qmm
@@ -190,6 +155,8 @@ using namespace qmm_host;
 namespace {
 
 bool i32(int64_t v) { return v >= 0 && v <= (int64_t)INT32_MAX; }
+// M rows of n elements, their rows padded, in fewer than 2^60 elements
+bool fits(int64_t M, int64_t n) { return M <= ((int64_t)1 << 59) / (n + 8); }
 
 // The rules shared by the gated block and the backward passes: affine
 // weights, 16-bit activations of the scales' dtype.
@@ -228,14 +195,13 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
   s = qmm_device_check();
   if (s != QMM_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
-  return launch_status(x_dtype == QMM_BF16
-                           ? qmm::ffn::forward_t<__nv_bfloat16>(x, M, K, gate, up, h, h_dtype, g_pre, u_pre, st)
-                           : qmm::ffn::forward_t<__half>(x, M, K, gate, up, h, h_dtype, g_pre, u_pre, st));
+  return launch_status(qmm::ffn::forward(x, x_dtype, M, K, gate, up, h, h_dtype, g_pre, u_pre, st));
 }
 
 int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (!i32(M) || !i32(K) || !i32(N)) return -1;
-  return 16;
+  if (!i32(M) || !i32(K) || !i32(N) || !fits(M, N)) return -1;
+  // rows of dy that do not start on 16 bytes are copied to ones that do
+  return 16 + (N % 8 ? M * qmm::ffn::padded(N) * 2 : 0);
 }
 
 qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype, int64_t M, int64_t K,
@@ -245,7 +211,8 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
   if (s != QMM_OK) return s;
   if (!dtype_ok(g_dtype) || (g_dtype != x_dtype && g_dtype != QMM_F32)) return QMM_ERR_DTYPE;
   if ((dscales == nullptr) != (dbiases == nullptr) || (!dx && !dscales)) return QMM_ERR_INVALID_ARG;
-  if (workspace_bytes < qmm_matmul_backward_workspace_bytes(M, K, w->rows)) return QMM_ERR_INVALID_ARG;
+  const int64_t need = qmm_matmul_backward_workspace_bytes(M, K, w->rows);
+  if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M > 0 && w->rows > 0 && (!aligned16(dy) || !aligned16(x))) return QMM_ERR_ALIGNMENT;
   if ((dx && !aligned16(dx)) || (dscales && (!aligned16(dscales) || !aligned16(dbiases))) || !aligned16(workspace))
     return QMM_ERR_ALIGNMENT;
@@ -253,15 +220,20 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
   if (s != QMM_OK) return s;
   void* const grads[4] = {dscales, dbiases, nullptr, nullptr};
   cudaStream_t st = (cudaStream_t)stream;
-  return launch_status(
-      x_dtype == QMM_BF16
-          ? qmm::ffn::backward_t<__nv_bfloat16>(dy, nullptr, x, M, K, w, nullptr, dx, grads, g_dtype, st)
-          : qmm::ffn::backward_t<__half>(dy, nullptr, x, M, K, w, nullptr, dx, grads, g_dtype, st));
+  const int64_t N = w->rows, ld = qmm::ffn::padded(N), n = M * N;
+  if (ld != N && n > 0) {
+    qmm::ffn::pad_kernel<<<qmm::ffn::blocks_for(n), 256, 0, st>>>((const uint16_t*)dy, n, (int)N, (int)ld,
+                                                                  (uint16_t*)workspace);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return launch_status(e);
+    dy = workspace;
+  }
+  return launch_status(qmm::ffn::backward(dy, nullptr, ld, x, x_dtype, M, K, w, nullptr, dx, grads, g_dtype, st));
 }
 
 int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F) {
-  if (!i32(M) || !i32(K) || !i32(F)) return -1;
-  return 16 + (M * F * 2 + 15) / 16 * 16 * 2;
+  if (!i32(M) || !i32(K) || !i32(F) || !fits(M, F)) return -1;
+  return 16 + 2 * M * qmm::ffn::padded(F) * 2;  // dg and du
 }
 
 qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* g_pre, const void* u_pre,
@@ -277,7 +249,8 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
     if ((grads[i] == nullptr) != (grads[0] == nullptr)) return QMM_ERR_INVALID_ARG;
   if (!dx && !grads[0]) return QMM_ERR_INVALID_ARG;
   const int64_t F = gate->rows;
-  if (workspace_bytes < qmm_gate_up_silu_backward_workspace_bytes(M, K, F)) return QMM_ERR_INVALID_ARG;
+  const int64_t need = qmm_gate_up_silu_backward_workspace_bytes(M, K, F);
+  if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M > 0 && F > 0 && (!aligned16(dh) || !aligned16(x) || !aligned16(g_pre) || !aligned16(u_pre)))
     return QMM_ERR_ALIGNMENT;
   if ((dx && !aligned16(dx)) || !aligned16(workspace)) return QMM_ERR_ALIGNMENT;
@@ -286,23 +259,24 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
   s = qmm_device_check();
   if (s != QMM_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
-  char* dg = static_cast<char*>(workspace);
-  char* du = dg + (M * F * 2 + 15) / 16 * 16;
-  const int64_t n = M * F;
+  const int64_t ld = qmm::ffn::padded(F), n = M * F;
+  uint16_t* dg = static_cast<uint16_t*>(workspace);
+  uint16_t* du = dg + M * ld;
   if (n > 0) {
-    const int grid = (int)std::min<int64_t>((n + 255) / 256, 148 * 16);
+    const int grid = qmm::ffn::blocks_for(n);
     if (x_dtype == QMM_BF16) {
       using T = __nv_bfloat16;
-      qmm::ffn::act_grad_kernel<T><<<grid, 256, 0, st>>>((const T*)dh, (const T*)g_pre, (const T*)u_pre, n, (T*)dg, (T*)du);
+      qmm::ffn::act_grad_kernel<T><<<grid, 256, 0, st>>>((const T*)dh, (const T*)g_pre, (const T*)u_pre, n, (int)F,
+                                                        (int)ld, (T*)dg, (T*)du);
     } else {
       using T = __half;
-      qmm::ffn::act_grad_kernel<T><<<grid, 256, 0, st>>>((const T*)dh, (const T*)g_pre, (const T*)u_pre, n, (T*)dg, (T*)du);
+      qmm::ffn::act_grad_kernel<T><<<grid, 256, 0, st>>>((const T*)dh, (const T*)g_pre, (const T*)u_pre, n, (int)F,
+                                                        (int)ld, (T*)dg, (T*)du);
     }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return launch_status(e);
   }
-  return launch_status(
-      x_dtype == QMM_BF16
-          ? qmm::ffn::backward_t<__nv_bfloat16>(dg, du, x, M, K, gate, up, dx, grads, g_dtype, st)
-          : qmm::ffn::backward_t<__half>(dg, du, x, M, K, gate, up, dx, grads, g_dtype, st));
+  return launch_status(qmm::ffn::backward(dg, du, ld, x, x_dtype, M, K, gate, up, dx, grads, g_dtype, st));
 }
 
 }  // extern "C"

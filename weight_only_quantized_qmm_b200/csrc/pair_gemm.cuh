@@ -1,0 +1,826 @@
+// Tensor-core products of packed weights for many tokens (tcgen05, sm_100a):
+//   FWD  g | u [m, n] = sum_k x[m, k] w_hat[n, k] of gate and up, then
+//        h = SiLU(g) * u                               (A = x, B = w_hat)
+//   DX   dx[m, k] = sum over n (and parts) of dy[m, n] w_hat[n, k]
+//                                                      (A = dy, B = w_hat^T)
+//   DP   dW[n, k] = sum_m dy[m, n] x[m, k], folded at once into
+//        dscales[n, j] = sum_{k in j} dW q, dbiases[n, j] = sum_{k in j} dW
+//                                                      (A = dy^T, B = x^T)
+//
+// Tokens (DP: weight rows) are the M side of the MMA, so that an accumulator
+// lane is one output row and its columns are contiguous in memory: 16-byte
+// stores, and a group's sum of DP stays in one thread.  256 accumulator
+// columns: FWD holds 128 columns of g and the same 128 of u, so SiLU(g) * u is
+// local to a thread.
+//
+// PAIR: two CTAs share one 256 x 256 tile (cta_group::2); each holds 128 rows
+// of A and half of B, so an SM reads and writes 64 KB of shared memory per
+// 64-deep step (512 tensor cycles) instead of the 96 KB of a 128 x 256 tile,
+// which is what bounds that tile.  Single: one CTA per 128 x 256 tile for few
+// tokens; a cluster of `splits` CTAs may share a tile by cutting the sum, and
+// joins its partial tiles through distributed shared memory in rank order.
+//
+// FWD and DX dequantize in the kernel: sixteen warps keep four units (32
+// codes of one row) in flight in registers, form (OFF + q) - OFF and one fused
+// q * s + z in the activations' type (one rounding), and write the swizzled
+// operand tile: K-major for FWD, MN-major for DX (the same packed rows, read
+// along their length both times).
+//
+// Warps: 0 TMA producer; 1 TMEM owner and MMA issuer (PAIR: of the leader
+// CTA); 2.. epilogue (4 warps, DP 8); then the 16 dequant warps.
+// Every wait is bounded; after one that gave up the tiles are written as NaN.
+#pragma once
+
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "mbarrier.cuh"
+
+namespace qmm {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder();
+
+namespace pg {
+
+enum Op { FWD = 0, DX = 1, DP = 2 };
+
+constexpr int kBK = 64;                  // depth of a step: 128 bytes of 16-bit values
+constexpr int kTile = 128 * kBK * 2;     // 128 x 64 operand tile: 16 KB
+constexpr int kDeqWarps = 16;
+constexpr uint32_t kSpins = 1u << 22;
+
+template <int OP, bool PAIR>
+struct Cfg {
+  static constexpr int EPI = OP == DP ? 8 : 4;                     // epilogue warps
+  static constexpr int DEQ = OP == DP ? 0 : kDeqWarps;
+  static constexpr int THREADS = (2 + EPI + DEQ) * 32;
+  static constexpr int A_BYTES = kTile;                            // 128 rows of A per CTA
+  static constexpr int B_BYTES = PAIR ? kTile : 2 * kTile;         // 128 or 256 of B
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = PAIR ? 6 : 4;
+  static constexpr int BAR0 = STAGES * STAGE;
+  static constexpr int SMEM = 1024 + BAR0 + 256;                   // + alignment slack, barriers
+  static_assert(OP != DP || PAIR, "DP runs on CTA pairs");
+  static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barriers, TMEM slot and abort flag");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(PAIR || 128 * 256 * 4 <= BAR0, "a partial tile fits the stages");
+};
+
+struct Weight {
+  const uint32_t* packed;
+  const void* scales;
+  const void* biases;
+};
+
+struct Args {
+  int M, K, N;            // tokens, weight columns, weight rows (of one part)
+  int parts;              // FWD: 2; DX, DP: 1 or 2
+  Weight w[2];
+  int lgs;                // log2 of the group size
+  int m_tiles, n_tiles;   // tiles along the output's rows and columns (DP: rows of one part)
+  int steps;              // 64-deep steps of the whole sum
+  int splits;             // CTAs that share a tile by cutting the sum (single)
+  void* out[4];           // FWD: h, g, u; DX: dx; DP: dscales, dbiases of both parts
+  int out_dtype;          // FWD: of h; DP
+  int f16;                // operands are f16 (otherwise bf16)
+};
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// as mbar_wait_abortable, acquiring what the other CTA of the pair released
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const int* abort_flag) {
+  for (uint32_t i = 0; i < kSpins; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 1023u) == 1023u && *reinterpret_cast<const volatile int*>(abort_flag)) return false;
+  }
+  return false;
+}
+template <bool PAIR>
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
+  if constexpr (PAIR)  // the barrier may be the leader CTA's
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(m), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+// Shared-memory descriptors of 128-byte swizzled 16-bit operands.
+//   K-major: rows of 64 k, 8-row groups 1024 bytes apart;
+//   MN-major: blocks of [64 k][64 rows], 8 k 1024 bytes apart (stride byte
+//   offset), blocks of 64 rows 8192 bytes apart (leading byte offset).
+template <bool MN>
+__device__ __forceinline__ uint64_t desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(MN ? 8192u >> 4 : 1u) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;  // descriptor version (sm_100)
+  d |= (uint64_t)2u << 61;  // 128-byte swizzle
+  return d;
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// arrives on `bar` (PAIR: of both CTAs) once the MMAs issued so far are done
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 16 columns of this warp's 32 lanes; tmem_wait() before the registers are read
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void sts_v4(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 lds_cluster(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+// ------------------------------------------------------------------ dequantize
+// 32 codes of one row (B words) and their group's scale and bias
+template <int B>
+struct Unit {
+  uint32_t w[B];
+  uint16_t s, z;
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __half>::value)
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __half>::value)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  else
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return (uint32_t)bits16(from_f32<T>(a)) | ((uint32_t)bits16(from_f32<T>(b)) << 16);
+}
+
+// Values 8c .. 8c + 7 of the unit as four pairs of T.
+template <int B, typename T>
+__device__ __forceinline__ uint4 dequant8(const Unit<B>& u, int c) {
+  constexpr bool H = std::is_same<T, __half>::value;
+  uint32_t v[4];
+  if constexpr (B == 8 && !H) {
+    // 8-bit codes do not fit under a bf16 magic: exact in fp32, one rounding
+    const float s = __uint_as_float((uint32_t)u.s << 16), z = __uint_as_float((uint32_t)u.z << 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w = u.w[2 * c + (e >> 1)];
+      const float q0 = __uint_as_float(__byte_perm(w, 0x4B000000u, (e & 1) ? 0x7442 : 0x7440)) - 8388608.0f;
+      const float q1 = __uint_as_float(__byte_perm(w, 0x4B000000u, (e & 1) ? 0x7443 : 0x7441)) - 8388608.0f;
+      v[e] = pack2<T>(fmaf(q0, s, z), fmaf(q1, s, z));
+    }
+  } else {
+    // (OFF + q) in T with the code in the low mantissa bits; minus OFF is exact
+    constexpr uint32_t OFF2 = H ? 0x64006400u : 0x43004300u;
+    const uint32_t s2 = (uint32_t)u.s * 0x00010001u, z2 = (uint32_t)u.z * 0x00010001u;
+    uint32_t p[4];
+    if constexpr (B == 8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = u.w[2 * c + (e >> 1)];
+        p[e] = __byte_perm(w, 0x64646464u, (e & 1) ? 0x4342 : 0x4140);
+      }
+    } else if constexpr (B == 4) {
+      const uint32_t w = u.w[c];
+      const uint32_t t0 = w & 0x0F0F0F0Fu, t1 = (w >> 4) & 0x0F0F0F0Fu;
+      const uint32_t a = __byte_perm(t0, t1, 0x5140), b = __byte_perm(t0, t1, 0x7362);
+      constexpr uint32_t M8 = H ? 0x64646464u : 0x43434343u;
+      p[0] = __byte_perm(a, M8, 0x4140);
+      p[1] = __byte_perm(a, M8, 0x4342);
+      p[2] = __byte_perm(b, M8, 0x4140);
+      p[3] = __byte_perm(b, M8, 0x4342);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        p[e] = stream_code<B>(u.w, 8 * c + 2 * e) | (stream_code<B>(u.w, 8 * c + 2 * e + 1) << 16) | OFF2;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = fma2<T>(sub2<T>(p[e], OFF2), s2, z2);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// the words of unit `src` (4 B bytes from the last one), read once: past L1
+template <int B>
+__device__ __forceinline__ void load_words(const uint32_t* src, uint32_t (&w)[B]) {
+  if constexpr (B % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < B; i += 4)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "l"(src + i));
+  } else if constexpr (B % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < B; i += 2)
+      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "l"(src + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[i]) : "l"(src + i));
+  }
+}
+
+struct Tile {
+  int m0, n0, part;  // first output row and column of the cluster's tile; DP: the part it belongs to
+};
+template <int OP, bool PAIR>
+__device__ __forceinline__ Tile tile_of(const Args& p, int t) {
+  constexpr int TM = PAIR ? 256 : 128;
+  constexpr int TN = OP == FWD ? 128 : 256;
+  // tiles along M vary fastest: the clusters running at one time share weight tiles
+  const int nt = t / p.m_tiles, mt = t - nt * p.m_tiles;
+  if constexpr (OP == DP) {
+    const int part = nt / p.n_tiles;
+    return Tile{mt * TM, (nt - part * p.n_tiles) * TN, part};
+  } else {
+    return Tile{mt * TM, nt * TN, 0};
+  }
+}
+
+// out[0 .. 7] of one row (16-byte aligned when vec), the first `cnt` of them
+template <typename T>
+__device__ __forceinline__ void store8(T* dst, const float* v, bool vec, int cnt) {
+  if (vec && cnt >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      *reinterpret_cast<uint4*>(dst) =
+          make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < cnt) dst[i] = from_f32<T>(v[i]);
+  }
+}
+
+// h (and g, u) of 8 columns from column n of row m
+template <typename T>
+__device__ __forceinline__ void store_h8(const Args& p, int m, int n, const float* g, const float* u, bool vec) {
+  const int cnt = p.N - n;
+  if (cnt <= 0) return;
+  const int64_t at = (int64_t)m * p.N + n;
+  float h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
+  if (p.out_dtype == QMM_F32)
+    store8(reinterpret_cast<float*>(p.out[0]) + at, h, vec, cnt);
+  else
+    store8(reinterpret_cast<T*>(p.out[0]) + at, h, vec, cnt);
+  if (p.out[1]) {
+    store8(reinterpret_cast<T*>(p.out[1]) + at, g, vec, cnt);
+    store8(reinterpret_cast<T*>(p.out[2]) + at, u, vec, cnt);
+  }
+}
+
+template <int OP, int B, typename T, bool PAIR>
+__global__ void __launch_bounds__(Cfg<OP, PAIR>::THREADS, 1)
+pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap tma0,
+                 const __grid_constant__ CUtensorMap tma1, const __grid_constant__ CUtensorMap tmb) {
+  using C = Cfg<OP, PAIR>;
+  constexpr int S = C::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t stage0 = su32(smem);
+  const uint32_t full0 = stage0 + C::BAR0;   // [S] operands of the stage are in (PAIR: the leader's counts both CTAs)
+  const uint32_t empty0 = full0 + 8 * S;     // [S] the MMAs that read the stage are done
+  const uint32_t accf0 = empty0 + 8 * S;     // [2] accumulator complete
+  const uint32_t tfree0 = accf0 + 16;        // [2] accumulator read out
+  const uint32_t drain = tfree0 + 16;        // every issued MMA complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR0 + 8 * (2 * S + 5));
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  const bool leader = !PAIR || rank == 0;
+  const int splits = PAIR ? 1 : p.splits;
+  const int cta_per = PAIR ? 2 : splits;  // CTAs of a cluster
+  const int cluster = blockIdx.x / cta_per, clusters = gridDim.x / cta_per;
+  const int split = PAIR ? 0 : (int)rank;
+  // this CTA's range of steps, and its cluster's tiles
+  const int s_lo = (int)((int64_t)p.steps * split / splits), s_hi = (int)((int64_t)p.steps * (split + 1) / splits);
+  const int nk = s_hi - s_lo;
+  const int T_all = p.m_tiles * p.n_tiles * (OP == DP ? p.parts : 1);
+  const int my_tiles = cluster < T_all ? (T_all - 1 - cluster) / clusters + 1 : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      // the producer, and the dequant warps that fill the stage (all 16 of a
+      // single CTA; 8 of each CTA of a pair, which take turns by stage)
+      mbar_init(full0 + 8 * s, 1 + (OP == DP ? 0 : kDeqWarps));
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf0 + 8 * b, 1);
+      mbar_init(tfree0 + 8 * b, C::EPI * (PAIR ? 2 : 1));
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {  // two accumulators of 256 columns
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTAs' barriers are initialised
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // the operands may come from the previous kernel
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      constexpr uint32_t kTx = (PAIR ? 2 : 1) * (OP == DP ? C::STAGE : C::A_BYTES);
+      const uint32_t lfull0 = PAIR ? map_rank(full0, 0) : full0;
+      const int half = OP == DP ? 0 : p.steps / p.parts;  // DX: steps of one part
+      int s = 0, u = 0, issued = 0;
+      bool stop = false;
+      for (int lt = 0; lt < my_tiles && !stop; ++lt) {
+        const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
+        const int row = tl.m0 + (PAIR ? 128 * (int)rank : 0);
+        for (int i = s_lo; i < s_hi; ++i) {
+          if (u > 0 && !mbar_wait_abortable(empty0 + 8 * s, (u - 1) & 1, kSpins, abort_flag)) {
+            *abort_flag = 1;
+            stop = true;
+            break;
+          }
+          const uint32_t a = stage0 + s * C::STAGE, bar = lfull0 + 8 * s;
+          if (leader) mbar_arrive_expect_tx(full0 + 8 * s, kTx);
+          if constexpr (OP == DP) {
+            const CUtensorMap* ma = tl.part ? &tma1 : &tma0;
+            const int col = tl.n0 + 128 * (int)rank;
+            tma_2d<PAIR>(a, ma, row, i * kBK, bar);
+            tma_2d<PAIR>(a + 8192, ma, row + 64, i * kBK, bar);
+            tma_2d<PAIR>(a + C::A_BYTES, &tmb, col, i * kBK, bar);
+            tma_2d<PAIR>(a + C::A_BYTES + 8192, &tmb, col + 64, i * kBK, bar);
+          } else if constexpr (OP == DX) {
+            const bool second = i >= half;
+            tma_2d<PAIR>(a, second ? &tma1 : &tma0, (second ? i - half : i) * kBK, row, bar);
+          } else {
+            tma_2d<PAIR>(a, &tma0, i * kBK, row, bar);
+          }
+          ++issued;
+          if (++s == S) s = 0, ++u;
+        }
+      }
+      // no copy may still be landing when the CTA exits.  Every copy of a
+      // finished tile was waited for by its MMAs; after a failure the leader
+      // waits for the stages it armed, and the other CTA, whose copies count on
+      // the leader's barrier, sits out a time far beyond any copy's.
+      if (*reinterpret_cast<volatile int*>(abort_flag)) {
+        if (leader) {
+          for (int i = max(0, issued - S); i < issued; ++i)
+            mbar_wait_n(full0 + 8 * (i % S), (uint32_t)(i / S) & 1u, 1u << 12);
+        }
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0 && leader) {
+      constexpr bool AMN = OP == DP, BMN = OP != FWD;
+      constexpr int AK = AMN ? 2048 : 32, BK_ = BMN ? 2048 : 32;  // bytes per 16 k
+      const uint32_t fmt = p.f16 ? 0u : 1u;
+      const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
+                             ((256u >> 3) << 17) | (((PAIR ? 256u : 128u) >> 4) << 24);
+      int s = 0, u = 0;
+      bool stop = false;
+      for (int lt = 0; lt < my_tiles && !stop; ++lt) {
+        const int b = lt & 1;
+        if (lt >= 2 && !wait_cluster(tfree0 + 8 * b, ((lt >> 1) - 1) & 1, abort_flag)) {
+          *abort_flag = 1;
+          break;
+        }
+        fence_after();
+        const uint32_t acc = tmem + (uint32_t)(b * 256);
+        for (int i = 0; i < nk; ++i) {
+          if (!wait_cluster(full0 + 8 * s, u & 1, abort_flag)) {
+            *abort_flag = 1;
+            stop = true;
+            break;
+          }
+          fence_after();
+          const uint32_t a0 = stage0 + s * C::STAGE, b0 = a0 + C::A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma<PAIR>(acc, desc<AMN>(a0 + kk * AK), desc<BMN>(b0 + kk * BK_), idesc, (i | kk) != 0 ? 1u : 0u);
+          commit<PAIR>(empty0 + 8 * s);
+          if (++s == S) s = 0, ++u;
+        }
+        commit<PAIR>(accf0 + 8 * b);  // (also after a failure)
+      }
+      // TMEM is released only once every issued MMA is done
+      commit<PAIR>(drain);
+      mbar_wait_n(drain, 0, kSpins);
+    }
+  } else if (warp < 2 + C::EPI) {
+    // ---------------- epilogue ----------------
+    const int qq = warp & 3;           // the TMEM lanes this warp may read
+    const int r = qq * 32 + lane;      // row of the CTA's 128
+    const uint32_t lanes = tmem + ((uint32_t)(qq * 32) << 16);
+    const uint32_t ltfree0 = PAIR ? map_rank(tfree0, 0) : tfree0;
+    const float nan = __int_as_float(0x7fc00000);
+    bool failed = false;
+    for (int lt = 0; lt < my_tiles; ++lt) {
+      const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
+      const int b = lt & 1;
+      if (!failed) {
+        failed = !mbar_wait_abortable(accf0 + 8 * b, (lt >> 1) & 1, kSpins, abort_flag) ||
+                 *reinterpret_cast<volatile int*>(abort_flag);
+        failed = __any_sync(0xffffffffu, failed);
+      }
+      fence_after();
+      const uint32_t acc = lanes + (uint32_t)(b * 256);
+      const int row = tl.m0 + (PAIR ? 128 * (int)rank : 0) + r;
+      if constexpr (OP == DP) {
+        // 128 columns of one weight row: units of 32, groups of 1, 2 or 4
+        const int c0 = ((warp - 2) >> 2) * 128;
+        const int lu = p.lgs - 5;  // log2 of the units per group
+        const int64_t G = p.K >> p.lgs;
+        const bool live = row < p.N;
+        float ds = 0.0f, dz = 0.0f;
+#pragma unroll
+        for (int un = 0; un < 4; ++un) {
+          const int k = tl.n0 + c0 + un * 32;
+          if (k < p.K) {
+            uint32_t w[B];
+            if (live) load_words<B>(p.w[tl.part].packed + ((int64_t)row * (p.K >> 5) + (k >> 5)) * B, w);
+            float sq = 0.0f, sv = 0.0f;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float v[16];
+              if (!failed) {
+                tmem_ld16(acc + (uint32_t)(c0 + un * 32 + hf * 16), v);
+                tmem_wait();
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = nan;
+              }
+              if (live) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  // q / 2^B: the code in the top mantissa bits of 1.0, less 1.0
+                  const uint32_t q = stream_code<B>(w, hf * 16 + i);
+                  sq = fmaf(v[i], __uint_as_float(0x3F800000u | (q << (23 - B))) - 1.0f, sq);
+                  sv += v[i];
+                }
+              }
+            }
+            ds += sq * (float)(1 << B);
+            dz += sv;
+            if (((un + 1) & ((1 << lu) - 1)) == 0) {
+              if (live) {
+                const int64_t at = (int64_t)row * G + (k >> p.lgs);
+                store_as(p.out[2 * tl.part], p.out_dtype, at, ds);
+                store_as(p.out[2 * tl.part + 1], p.out_dtype, at, dz);
+              }
+              ds = dz = 0.0f;
+            }
+          }
+        }
+      } else if (splits > 1) {
+        // a partial tile: four columns of all 128 rows are 2 KB
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 16) {
+          float v[16];
+          if (!failed) {
+            tmem_ld16(acc + (uint32_t)c, v);
+            tmem_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = nan;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sts_v4(stage0 + (uint32_t)(((c >> 2) + i) * 2048 + r * 16),
+                   make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                              __float_as_uint(v[4 * i + 3])));
+        }
+      } else if constexpr (OP == FWD) {
+        const bool vec = p.N % 8 == 0;
+#pragma unroll 1
+        for (int c = 0; c < 128 && tl.n0 + c < p.N; c += 16) {
+          float g[16], u[16];
+          if (!failed) {
+            tmem_ld16(acc + (uint32_t)c, g);
+            tmem_ld16(acc + (uint32_t)(128 + c), u);
+            tmem_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] = u[i] = nan;
+          }
+          if (row < p.M) {
+            store_h8<T>(p, row, tl.n0 + c, g, u, vec);
+            store_h8<T>(p, row, tl.n0 + c + 8, g + 8, u + 8, vec);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 256 && tl.n0 + c < p.K; c += 16) {
+          float v[16];
+          if (!failed) {
+            tmem_ld16(acc + (uint32_t)c, v);
+            tmem_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = nan;
+          }
+          if (row < p.M) {
+            T* dst = reinterpret_cast<T*>(p.out[0]) + (int64_t)row * p.K + tl.n0 + c;
+            store8(dst, v, true, 8);
+            store8(dst + 8, v + 8, true, 8);
+          }
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0 && !failed) {
+        if constexpr (PAIR)
+          arrive_remote(ltfree0 + 8 * b);
+        else
+          mbar_arrive(tfree0 + 8 * b);
+      }
+    }
+  } else if constexpr (OP != DP) {
+    // ---------------- dequantize ----------------
+    constexpr int kAhead = B == 8 ? 2 : 4;  // units in flight per thread
+    constexpr int STEP = PAIR ? 2 : 1;      // a pair's two sets of 8 warps take turns by stage
+    const int dw = warp - 2 - C::EPI;
+    const uint32_t lfull0 = PAIR ? map_rank(full0, 0) : full0;
+    const int wpr = (p.K >> 5) * B;
+    const int64_t G = p.K >> p.lgs;
+    const int half = p.steps / p.parts;
+    // this thread's unit in a stage and its 16-byte chunks in the operand tile.
+    // Lanes are laid so that eight consecutive ones write eight different bank
+    // groups, and the lanes that share a row read one 32-byte piece of it.
+    int ur, uc;          // FWD: row of the 128 (256) and which half of its 64 codes
+    uint32_t at;         // byte offset of chunk 0 before the swizzle
+    int swz;
+    if constexpr (OP == FWD) {
+      ur = (PAIR ? dw & 7 : dw) * 16 + (lane >> 1);
+      uc = lane & 1;
+      at = (uint32_t)(ur * 128);
+      swz = ur & 7;
+    } else {             // DX: row of the 64 and which 32 of the tile's columns
+      ur = (dw & 7) * 8 + ((lane >> 1) & 3) + ((lane >> 4) << 2);
+      uc = (lane & 1) | ((lane >> 3) & 1) << 1 | (PAIR ? 0 : (dw >> 3) << 2);
+      at = (uint32_t)((uc >> 1) * 8192 + ur * 128);
+      swz = ur & 7;
+    }
+    const int ch0 = (uc & 1) * 4;  // first chunk of the unit in its 128 bytes
+
+    // the cursor of the loads: step i of tile lt
+    int li = PAIR ? (dw >> 3) : 0, llt = 0;
+    Tile ltl{};
+    auto settle = [&]() {
+      while (li >= nk && llt < my_tiles) li -= nk, ++llt;
+      if (llt < my_tiles) ltl = tile_of<OP, PAIR>(p, cluster + llt * clusters);
+    };
+    auto load = [&](Unit<B>& un) {
+      bool ok = llt < my_tiles;
+      const int i = s_lo + li;
+      int64_t row;
+      int k, part;
+      if constexpr (OP == FWD) {
+        row = ltl.n0 + (ur & 127);
+        part = PAIR ? (int)rank : ur >> 7;
+        k = i * kBK + uc * 32;
+      } else {
+        part = i >= half ? 1 : 0;
+        row = (int64_t)(part ? i - half : i) * kBK + ur;
+        k = ltl.n0 + (PAIR ? 128 * (int)rank : 0) + uc * 32;
+      }
+      ok = ok && row < p.N && k < p.K;
+      if (ok) {
+        const Weight& w = p.w[part];
+        load_words<B>(w.packed + row * wpr + (k >> 5) * B, un.w);
+        un.s = __ldg(reinterpret_cast<const uint16_t*>(w.scales) + row * G + (k >> p.lgs));
+        un.z = __ldg(reinterpret_cast<const uint16_t*>(w.biases) + row * G + (k >> p.lgs));
+      } else {  // past the weight: zeros, which the sum's padding is multiplied by
+#pragma unroll
+        for (int j = 0; j < B; ++j) un.w[j] = 0u;
+        un.s = un.z = 0;
+      }
+      li += STEP;
+      if (li >= nk) settle();
+    };
+    settle();
+    Unit<B> ring[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) load(ring[a]);
+    const int total = my_tiles * nk;
+    for (int j0 = PAIR ? (dw >> 3) : 0; j0 < total; j0 += STEP * kAhead) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int j = j0 + a * STEP;
+        if (j < total) {
+          const int s = j % S, u = j / S;
+          if (u > 0 && !mbar_wait_abortable(empty0 + 8 * s, (u - 1) & 1, kSpins, abort_flag)) *abort_flag = 1;
+          const uint32_t dst = stage0 + (uint32_t)(s * C::STAGE + C::A_BYTES) + at;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sts_v4(dst + (uint32_t)(((ch0 + c) ^ swz) << 4), dequant8<B, T>(ring[a], c));
+          load(ring[a]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR)
+              arrive_remote(lfull0 + 8 * s);
+            else
+              mbar_arrive(full0 + 8 * s);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  fence_before();
+  if constexpr (OP != DP && !PAIR) {
+    if (splits > 1) {
+      // join the partial tiles: this CTA takes its share of the columns of all
+      // rows, adding the CTAs' partials in rank order
+      cluster_sync();
+      constexpr int COLS = OP == FWD ? 128 : 256;
+      const Tile tl = tile_of<OP, PAIR>(p, cluster);
+      const int per = COLS / 8 / splits;  // 8-column pieces of this CTA (splits divides 16)
+      const bool vec = OP == DX || p.N % 8 == 0;
+      const int rows = min(128, p.M - tl.m0);
+      for (int it = threadIdx.x; it < per * 128; it += C::THREADS) {
+        const int row = it & 127, c = ((int)rank * per + (it >> 7)) * 8;
+        if (row >= rows || tl.n0 + c >= (OP == FWD ? p.N : p.K)) continue;
+        float v[2][8];
+#pragma unroll
+        for (int q = 0; q < (OP == FWD ? 2 : 1); ++q) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
+          for (int src = 0; src < splits; ++src) {
+            const uint32_t a = map_rank(stage0 + (uint32_t)(((q * 128 + c) >> 2) * 2048 + row * 16), src);
+            const float4 x = lds_cluster(a), y = lds_cluster(a + 2048);
+            v[q][0] += x.x; v[q][1] += x.y; v[q][2] += x.z; v[q][3] += x.w;
+            v[q][4] += y.x; v[q][5] += y.y; v[q][6] += y.z; v[q][7] += y.w;
+          }
+        }
+        if constexpr (OP == FWD)
+          store_h8<T>(p, tl.m0 + row, tl.n0 + c, v[0], v[1], vec);
+        else
+          store8(reinterpret_cast<T*>(p.out[0]) + (int64_t)(tl.m0 + row) * p.K + tl.n0 + c, v[0], true, 8);
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while another may signal or read it
+  if (warp == 1) {
+    fence_after();
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ------------------------------------------------------------------ host
+// 2-D map over 16-bit [rows, cols] (row stride ld elements): boxes of 64
+// columns x box_rows rows, 128-byte swizzle, zeros outside
+inline bool make_map(CUtensorMap* m, const void* base, bool f16, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
+  const cuuint32_t box[2] = {kBK, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int OP, int B, typename T, bool PAIR>
+cudaError_t launch(const Args& p, const CUtensorMap (&tm)[3], int clusters, cudaStream_t st) {
+  using C = Cfg<OP, PAIR>;
+  auto k = pair_gemm_kernel<OP, B, T, PAIR>;
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    configured[dev] = 1;
+  }
+  const int per = PAIR ? 2 : p.splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * per);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = per;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, p, tm[0], tm[1], tm[2]);
+}
+
+// One bit width's kernels; DP does not depend on T.
+template <int B>
+cudaError_t dispatch(int op, bool pair, const Args& p, const CUtensorMap (&tm)[3], int clusters, cudaStream_t st) {
+  if (op == DP) return launch<DP, B, __nv_bfloat16, true>(p, tm, clusters, st);
+  if (op == FWD) {
+    if (p.f16)
+      return pair ? launch<FWD, B, __half, true>(p, tm, clusters, st) : launch<FWD, B, __half, false>(p, tm, clusters, st);
+    return pair ? launch<FWD, B, __nv_bfloat16, true>(p, tm, clusters, st)
+                : launch<FWD, B, __nv_bfloat16, false>(p, tm, clusters, st);
+  }
+  if (p.f16)
+    return pair ? launch<DX, B, __half, true>(p, tm, clusters, st) : launch<DX, B, __half, false>(p, tm, clusters, st);
+  return pair ? launch<DX, B, __nv_bfloat16, true>(p, tm, clusters, st)
+              : launch<DX, B, __nv_bfloat16, false>(p, tm, clusters, st);
+}
+
+}  // namespace pg
+}  // namespace qmm

@@ -1,0 +1,12 @@
+// Instantiations of the many-token products of packed weights for 3-bit codes.
+#include "pair_gemm.cuh"
+
+namespace qmm {
+namespace pg {
+
+cudaError_t dispatch_b3(int op, bool pair, const Args& p, const CUtensorMap (&tm)[3], int clusters, cudaStream_t st) {
+  return dispatch<3>(op, pair, p, tm, clusters, st);
+}
+
+}  // namespace pg
+}  // namespace qmm
