@@ -449,6 +449,11 @@ qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int3
                                   qmm_dtype g_dtype, void* workspace, int64_t workspace_bytes, int32_t* d_status,
                                   void* stream);
 
+/* Workspace bytes of qmm_gate_up_silu (-1 for a size outside [0, 2^31 - 1] or
+ * M * F or F * K past 2^57): room for both dequantized weights for many
+ * tokens, 16 bytes otherwise. */
+int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F);
+
 /* The gated projection: h[M, F] = SiLU(x . dequant(gate)^T) * (x .
  * dequant(up)^T), SiLU(g) = g / (1 + exp(-g)): the dense form of
  * qmm_moe_gemv_id_gate_up_silu, for any number of tokens.  gate and up: [F, K]
@@ -456,14 +461,14 @@ qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int3
  * (both NULL, or both [M, F] in x_dtype) receive the two projections, which
  * the backward pass reads.  M == 0 or F == 0 is a no-op.
  * Errors: INVALID_ARG (shape rules, K, gate and up differ, one of g_pre and
- * u_pre missing), UNSUPPORTED (see above, sizes past 2^31 - 1, device), DTYPE,
- * ALIGNMENT (x, h, g_pre, u_pre 16-byte), CUDA. */
+ * u_pre missing, workspace_bytes), UNSUPPORTED (see above, sizes past 2^31 - 1,
+ * device), DTYPE, ALIGNMENT (x, h, g_pre, u_pre, workspace 16-byte), CUDA. */
 qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
                             const qmm_qweight* up, void* h, qmm_dtype h_dtype, void* g_pre, void* u_pre,
-                            void* stream);
+                            void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1]
- * or M * N past 2^59). */
+ * or M * N or N * K past 2^57). */
 int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
 /* Gradients of y = x . dequant(W)^T (qmm_matmul, transpose = 1): dx[M, K] = dy .
@@ -478,7 +483,7 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of qmm_gate_up_silu_backward (-1 for a size outside
- * [0, 2^31 - 1] or M * F past 2^59). */
+ * [0, 2^31 - 1] or M * F or F * K past 2^57). */
 int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F);
 
 /* Gradients of the gated projection from its saved g_pre and u_pre: with

@@ -56,23 +56,24 @@ def test_embedding_backward(L):
 
 
 def test_gate_up(L):
-    def call(g=None, u=None, x=A, xt=BF, M=2, K=128, h=A, ht=BF, gp=None, up=None):
+    def call(g=None, u=None, x=A, xt=BF, M=2, K=128, h=A, ht=BF, gp=None, up=None, ws=A, nb=1 << 40):
         g, u = g or qw(), u or qw()
-        return L.qmm_gate_up_silu(x, xt, M, K, ctypes.byref(g), ctypes.byref(u), h, ht, gp, up, None)
+        return L.qmm_gate_up_silu(x, xt, M, K, ctypes.byref(g), ctypes.byref(u), h, ht, gp, up, ws, nb, None)
 
     assert call(M=0) == _lib.QMM_OK
-    assert call(M=-1) == call(K=64) == call(gp=A) == call(up=A) == _lib.QMM_ERR_INVALID_ARG
+    assert call(M=-1) == call(K=64) == call(gp=A) == call(up=A) == call(nb=0) == _lib.QMM_ERR_INVALID_ARG
     for other in (qw(rows=16), qw(bits=8), qw(gs=32), qw(cols=64)):
         assert call(u=other) == _lib.QMM_ERR_INVALID_ARG
     assert call(xt=HF) == call(ht=HF) == call(u=qw(sdtype=HF)) == _lib.QMM_ERR_DTYPE
     f = qw(sdtype=F32)
     assert call(f, f, xt=F32, ht=F32) == call(mx(), mx()) == call(M=2 ** 31) == _lib.QMM_ERR_UNSUPPORTED
-    for bad in (dict(x=A + 2), dict(h=A + 8), dict(x=0), dict(gp=A + 2, up=A), dict(gp=A, up=A + 2)):
+    for bad in (dict(x=A + 2), dict(h=A + 8), dict(x=0), dict(ws=A + 2), dict(ws=None), dict(gp=A + 2, up=A), dict(gp=A, up=A + 2)):
         assert call(**bad) == _lib.QMM_ERR_ALIGNMENT, bad
 
 
 def test_backward(L):
-    for need in (L.qmm_matmul_backward_workspace_bytes, L.qmm_gate_up_silu_backward_workspace_bytes):
+    for need in (L.qmm_matmul_backward_workspace_bytes, L.qmm_gate_up_silu_backward_workspace_bytes,
+                 L.qmm_gate_up_silu_workspace_bytes):
         assert need(0, 32, 0) >= 0 and need(100, 128, 77) >= 0
         assert need(-1, 128, 8) == need(8, 2 ** 31, 8) == need(8, 128, -1) == -1
 

@@ -35,7 +35,7 @@ EXPORTS = (
     "qmm_selftest_bounded_wait", "qmm_matmul_parts", "qmm_quantize_dynamic_int8",
     "qmm_dequantize_dynamic_int8", "qmm_matmul_dynamic_int8", "qmm_moe_gemm_workspace_bytes_gathered",
     "qmm_embedding", "qmm_embedding_backward_workspace_bytes", "qmm_embedding_backward",
-    "qmm_gate_up_silu", "qmm_matmul_backward_workspace_bytes", "qmm_matmul_backward",
+    "qmm_gate_up_silu_workspace_bytes", "qmm_gate_up_silu", "qmm_matmul_backward_workspace_bytes", "qmm_matmul_backward",
     "qmm_gate_up_silu_backward_workspace_bytes", "qmm_gate_up_silu_backward",
 )
 
@@ -122,7 +122,9 @@ def load() -> ctypes.CDLL:
     L.qmm_embedding_backward_workspace_bytes.restype = i64
     L.qmm_embedding_backward.argtypes = [vp, c_int, vp, i64, qwp, ctypes.c_float, vp, vp, c_int, vp, i64, vp, vp]
     L.qmm_embedding_backward.restype = c_int
-    L.qmm_gate_up_silu.argtypes = [vp, c_int, i64, i64, qwp, qwp, vp, c_int, vp, vp, vp]
+    L.qmm_gate_up_silu_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qmm_gate_up_silu_workspace_bytes.restype = i64
+    L.qmm_gate_up_silu.argtypes = [vp, c_int, i64, i64, qwp, qwp, vp, c_int, vp, vp, vp, i64, vp]
     L.qmm_gate_up_silu.restype = c_int
     L.qmm_matmul_backward_workspace_bytes.argtypes = [i64, i64, i64]
     L.qmm_matmul_backward_workspace_bytes.restype = i64

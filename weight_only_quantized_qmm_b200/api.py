@@ -720,7 +720,7 @@ def qmm_embedding_backward(dy: torch.Tensor, ids: torch.Tensor, qw: QWeight, alp
 
 
 def qmm_gate_up_silu(x: torch.Tensor, gate: QWeight, up: QWeight, y_dtype: torch.dtype | None = None, out=None,
-                     save: bool = False, g_pre=None, u_pre=None, stream=None):
+                     save: bool = False, g_pre=None, u_pre=None, workspace=None, stream=None):
     """h = SiLU(x . dequant(gate)^T) * (x . dequant(up)^T); x [..., K], h [..., F].
     With save (or g_pre and u_pre given) returns (h, g, u), the projections
     in x's dtype that qmm_gate_up_silu_backward reads."""
@@ -732,10 +732,12 @@ def qmm_gate_up_silu(x: torch.Tensor, gate: QWeight, up: QWeight, y_dtype: torch
     if save or g_pre is not None or u_pre is not None:
         g_pre = _exactly(g_pre, "g_pre", (*lead, F), (x.dtype,), x2.device, stream)
         u_pre = _exactly(u_pre, "u_pre", (*lead, F), (x.dtype,), x2.device, stream)
-    cg, cu = _weights_here("qmm_gate_up_silu", {"x": x2, "out": out, "g_pre": g_pre, "u_pre": u_pre},
+    L = _lib.load()
+    ws = _workspace("qmm_gate_up_silu", workspace, L.qmm_gate_up_silu_workspace_bytes(M, K, F), x2.device, stream)
+    cg, cu = _weights_here("qmm_gate_up_silu", {"x": x2, "out": out, "g_pre": g_pre, "u_pre": u_pre, "workspace": ws},
                            {"gate": gate, "up": up})
-    rc = _lib.load().qmm_gate_up_silu(_ptr(x2), dtype_code(x2.dtype), M, K, ctypes.byref(cg), ctypes.byref(cu),
-                                      _ptr(out), dtype_code(out.dtype), _ptr(g_pre), _ptr(u_pre), _stream(stream))
+    rc = L.qmm_gate_up_silu(_ptr(x2), dtype_code(x2.dtype), M, K, ctypes.byref(cg), ctypes.byref(cu), _ptr(out),
+                            dtype_code(out.dtype), _ptr(g_pre), _ptr(u_pre), _ptr(ws), _nbytes(ws), _stream(stream))
     check("qmm_gate_up_silu", rc)
     return out if g_pre is None else (out, g_pre, u_pre)
 

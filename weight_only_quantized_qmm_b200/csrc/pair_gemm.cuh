@@ -20,7 +20,9 @@
 // tokens; a cluster of `splits` CTAs may share a tile by cutting the sum, and
 // joins its partial tiles through distributed shared memory in rank order.
 //
-// FWD and DX dequantize in the kernel: sixteen warps keep four units (32
+// FWD and DX take weights dequantized beforehand (B = 0: many tokens, where the
+// extra pass is small beside the product and the two TMA-fed operands run at
+// the tensor cores' rate), or dequantize in the kernel: sixteen warps keep four units (32
 // codes of one row) in flight in registers, form (OFF + q) - OFF and one fused
 // q * s + z in the activations' type (one rounding), and write the swizzled
 // operand tile: K-major for FWD, MN-major for DX (the same packed rows, read
@@ -54,10 +56,12 @@ constexpr int kTile = 128 * kBK * 2;     // 128 x 64 operand tile: 16 KB
 constexpr int kDeqWarps = 16;
 constexpr uint32_t kSpins = 1u << 22;
 
-template <int OP, bool PAIR>
+// The widths of FWD and DX, with B = 0 for weights dequantized beforehand.
+template <int OP, int B, bool PAIR>
 struct Cfg {
+  static constexpr bool DENSE = OP == DP || B == 0;                // both operands come by TMA
   static constexpr int EPI = OP == DP ? 8 : 4;                     // epilogue warps
-  static constexpr int DEQ = OP == DP ? 0 : kDeqWarps;
+  static constexpr int DEQ = DENSE ? 0 : kDeqWarps;
   static constexpr int THREADS = (2 + EPI + DEQ) * 32;
   static constexpr int A_BYTES = kTile;                            // 128 rows of A per CTA
   static constexpr int B_BYTES = PAIR ? kTile : 2 * kTile;         // 128 or 256 of B
@@ -65,7 +69,7 @@ struct Cfg {
   static constexpr int STAGES = PAIR ? 6 : 4;
   static constexpr int BAR0 = STAGES * STAGE;
   static constexpr int SMEM = 1024 + BAR0 + 256;                   // + alignment slack, barriers
-  static_assert(OP != DP || PAIR, "DP runs on CTA pairs");
+  static_assert(!DENSE || PAIR, "these run on CTA pairs");
   static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barriers, TMEM slot and abort flag");
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(PAIR || 128 * 256 * 4 <= BAR0, "a partial tile fits the stages");
@@ -105,8 +109,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t a, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Arrives on a barrier of the pair's leader.  What it announces is shared
+// memory of its own SM already made visible to the tensor cores by a proxy
+// fence, or TMEM reads already waited for, so it releases at CTA scope: a
+// cluster-scope release waits for every load in flight (measured at 1024 tokens
+// of 4096 x 14336: 347 us instead of 225).
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // as mbar_wait_abortable, acquiring what the other CTA of the pair released
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const int* abort_flag) {
@@ -227,35 +236,34 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return (uint32_t)bits16(from_f32<T>(a)) | ((uint32_t)bits16(from_f32<T>(b)) << 16);
 }
 
-// Values 8c .. 8c + 7 of the unit as four pairs of T.
+// Values 8c .. 8c + 7 of 32 codes as four pairs of T.
 template <int B, typename T>
-__device__ __forceinline__ uint4 dequant8(const Unit<B>& u, int c) {
+__device__ __forceinline__ uint4 dequant8(const uint32_t (&w)[B], uint16_t scale, uint16_t bias, int c) {
   constexpr bool H = std::is_same<T, __half>::value;
   uint32_t v[4];
   if constexpr (B == 8 && !H) {
     // 8-bit codes do not fit under a bf16 magic: exact in fp32, one rounding
-    const float s = __uint_as_float((uint32_t)u.s << 16), z = __uint_as_float((uint32_t)u.z << 16);
+    const float s = __uint_as_float((uint32_t)scale << 16), z = __uint_as_float((uint32_t)bias << 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t w = u.w[2 * c + (e >> 1)];
-      const float q0 = __uint_as_float(__byte_perm(w, 0x4B000000u, (e & 1) ? 0x7442 : 0x7440)) - 8388608.0f;
-      const float q1 = __uint_as_float(__byte_perm(w, 0x4B000000u, (e & 1) ? 0x7443 : 0x7441)) - 8388608.0f;
+      const uint32_t v4 = w[2 * c + (e >> 1)];
+      const float q0 = __uint_as_float(__byte_perm(v4, 0x4B000000u, (e & 1) ? 0x7442 : 0x7440)) - 8388608.0f;
+      const float q1 = __uint_as_float(__byte_perm(v4, 0x4B000000u, (e & 1) ? 0x7443 : 0x7441)) - 8388608.0f;
       v[e] = pack2<T>(fmaf(q0, s, z), fmaf(q1, s, z));
     }
   } else {
     // (OFF + q) in T with the code in the low mantissa bits; minus OFF is exact
     constexpr uint32_t OFF2 = H ? 0x64006400u : 0x43004300u;
-    const uint32_t s2 = (uint32_t)u.s * 0x00010001u, z2 = (uint32_t)u.z * 0x00010001u;
+    const uint32_t s2 = (uint32_t)scale * 0x00010001u, z2 = (uint32_t)bias * 0x00010001u;
     uint32_t p[4];
     if constexpr (B == 8) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t w = u.w[2 * c + (e >> 1)];
-        p[e] = __byte_perm(w, 0x64646464u, (e & 1) ? 0x4342 : 0x4140);
+        const uint32_t v4 = w[2 * c + (e >> 1)];
+        p[e] = __byte_perm(v4, 0x64646464u, (e & 1) ? 0x4342 : 0x4140);
       }
     } else if constexpr (B == 4) {
-      const uint32_t w = u.w[c];
-      const uint32_t t0 = w & 0x0F0F0F0Fu, t1 = (w >> 4) & 0x0F0F0F0Fu;
+      const uint32_t t0 = w[c] & 0x0F0F0F0Fu, t1 = (w[c] >> 4) & 0x0F0F0F0Fu;
       const uint32_t a = __byte_perm(t0, t1, 0x5140), b = __byte_perm(t0, t1, 0x7362);
       constexpr uint32_t M8 = H ? 0x64646464u : 0x43434343u;
       p[0] = __byte_perm(a, M8, 0x4140);
@@ -265,7 +273,7 @@ __device__ __forceinline__ uint4 dequant8(const Unit<B>& u, int c) {
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        p[e] = stream_code<B>(u.w, 8 * c + 2 * e) | (stream_code<B>(u.w, 8 * c + 2 * e + 1) << 16) | OFF2;
+        p[e] = stream_code<B>(w, 8 * c + 2 * e) | (stream_code<B>(w, 8 * c + 2 * e + 1) << 16) | OFF2;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = fma2<T>(sub2<T>(p[e], OFF2), s2, z2);
@@ -273,7 +281,7 @@ __device__ __forceinline__ uint4 dequant8(const Unit<B>& u, int c) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// the words of unit `src` (4 B bytes from the last one), read once: past L1
+// 32 codes, read once: past L1
 template <int B>
 __device__ __forceinline__ void load_words(const uint32_t* src, uint32_t (&w)[B]) {
   if constexpr (B % 4 == 0) {
@@ -348,10 +356,11 @@ __device__ __forceinline__ void store_h8(const Args& p, int m, int n, const floa
 }
 
 template <int OP, int B, typename T, bool PAIR>
-__global__ void __launch_bounds__(Cfg<OP, PAIR>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<OP, B, PAIR>::THREADS, 1)
 pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap tma0,
-                 const __grid_constant__ CUtensorMap tma1, const __grid_constant__ CUtensorMap tmb) {
-  using C = Cfg<OP, PAIR>;
+                 const __grid_constant__ CUtensorMap tma1, const __grid_constant__ CUtensorMap tmb0,
+                 const __grid_constant__ CUtensorMap tmb1) {
+  using C = Cfg<OP, B, PAIR>;
   constexpr int S = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
@@ -381,7 +390,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
     for (int s = 0; s < S; ++s) {
       // the producer, and the dequant warps that fill the stage (all 16 of a
       // single CTA; 8 of each CTA of a pair, which take turns by stage)
-      mbar_init(full0 + 8 * s, 1 + (OP == DP ? 0 : kDeqWarps));
+      mbar_init(full0 + 8 * s, 1 + (C::DENSE ? 0 : kDeqWarps));
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -413,7 +422,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
-      constexpr uint32_t kTx = (PAIR ? 2 : 1) * (OP == DP ? C::STAGE : C::A_BYTES);
+      constexpr uint32_t kTx = (PAIR ? 2 : 1) * (C::DENSE ? C::STAGE : C::A_BYTES);
       const uint32_t lfull0 = PAIR ? map_rank(full0, 0) : full0;
       const int half = OP == DP ? 0 : p.steps / p.parts;  // DX: steps of one part
       int s = 0, u = 0, issued = 0;
@@ -434,13 +443,21 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
             const int col = tl.n0 + 128 * (int)rank;
             tma_2d<PAIR>(a, ma, row, i * kBK, bar);
             tma_2d<PAIR>(a + 8192, ma, row + 64, i * kBK, bar);
-            tma_2d<PAIR>(a + C::A_BYTES, &tmb, col, i * kBK, bar);
-            tma_2d<PAIR>(a + C::A_BYTES + 8192, &tmb, col + 64, i * kBK, bar);
+            tma_2d<PAIR>(a + C::A_BYTES, &tmb0, col, i * kBK, bar);
+            tma_2d<PAIR>(a + C::A_BYTES + 8192, &tmb0, col + 64, i * kBK, bar);
           } else if constexpr (OP == DX) {
             const bool second = i >= half;
-            tma_2d<PAIR>(a, second ? &tma1 : &tma0, (second ? i - half : i) * kBK, row, bar);
+            const int n = (second ? i - half : i) * kBK;
+            tma_2d<PAIR>(a, second ? &tma1 : &tma0, n, row, bar);
+            if constexpr (C::DENSE) {
+              const CUtensorMap* mb = second ? &tmb1 : &tmb0;
+              const int col = tl.n0 + 128 * (int)rank;
+              tma_2d<PAIR>(a + C::A_BYTES, mb, col, n, bar);
+              tma_2d<PAIR>(a + C::A_BYTES + 8192, mb, col + 64, n, bar);
+            }
           } else {
             tma_2d<PAIR>(a, &tma0, i * kBK, row, bar);
+            if constexpr (C::DENSE) tma_2d<PAIR>(a + C::A_BYTES, rank ? &tmb1 : &tmb0, i * kBK, tl.n0, bar);
           }
           ++issued;
           if (++s == S) s = 0, ++u;
@@ -561,7 +578,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
             }
           }
         }
-      } else if (splits > 1) {
+      } else if (!PAIR && splits > 1) {
         // a partial tile: four columns of all 128 rows are 2 KB
 #pragma unroll 1
         for (int c = 0; c < 256; c += 16) {
@@ -624,7 +641,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
           mbar_arrive(tfree0 + 8 * b);
       }
     }
-  } else if constexpr (OP != DP) {
+  } else if constexpr (!C::DENSE) {
     // ---------------- dequantize ----------------
     constexpr int kAhead = B == 8 ? 2 : 4;  // units in flight per thread
     constexpr int STEP = PAIR ? 2 : 1;      // a pair's two sets of 8 warps take turns by stage
@@ -701,8 +718,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
           if (u > 0 && !mbar_wait_abortable(empty0 + 8 * s, (u - 1) & 1, kSpins, abort_flag)) *abort_flag = 1;
           const uint32_t dst = stage0 + (uint32_t)(s * C::STAGE + C::A_BYTES) + at;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) sts_v4(dst + (uint32_t)(((ch0 + c) ^ swz) << 4), dequant8<B, T>(ring[a], c));
-          load(ring[a]);
+          for (int c = 0; c < 4; ++c) sts_v4(dst + (uint32_t)(((ch0 + c) ^ swz) << 4), dequant8<B, T>(ring[a].w, ring[a].s, ring[a].z, c));
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
           __syncwarp();
           if (lane == 0) {
@@ -711,6 +727,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
             else
               mbar_arrive(full0 + 8 * s);
           }
+          load(ring[a]);
         }
       }
     }
@@ -718,7 +735,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
 
   __syncwarp();
   fence_before();
-  if constexpr (OP != DP && !PAIR) {
+  if constexpr (!PAIR) {
     if (splits > 1) {
       // join the partial tiles: this CTA takes its share of the columns of all
       // rows, adding the CTAs' partials in rank order
@@ -777,8 +794,8 @@ inline bool make_map(CUtensorMap* m, const void* base, bool f16, int64_t rows, i
 }
 
 template <int OP, int B, typename T, bool PAIR>
-cudaError_t launch(const Args& p, const CUtensorMap (&tm)[3], int clusters, cudaStream_t st) {
-  using C = Cfg<OP, PAIR>;
+cudaError_t launch(const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
+  using C = Cfg<OP, B, PAIR>;
   auto k = pair_gemm_kernel<OP, B, T, PAIR>;
   static int configured[64] = {0};
   int dev = 0;
@@ -803,23 +820,21 @@ cudaError_t launch(const Args& p, const CUtensorMap (&tm)[3], int clusters, cuda
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, p, tm[0], tm[1], tm[2]);
+  return cudaLaunchKernelEx(&cfg, k, p, tm[0], tm[1], tm[2], tm[3]);
+}
+
+template <int OP, int B, bool PAIR>
+cudaError_t launch_t(const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
+  return p.f16 ? launch<OP, B, __half, PAIR>(p, tm, clusters, st)
+               : launch<OP, B, __nv_bfloat16, PAIR>(p, tm, clusters, st);
 }
 
 // One bit width's kernels; DP does not depend on T.
 template <int B>
-cudaError_t dispatch(int op, bool pair, const Args& p, const CUtensorMap (&tm)[3], int clusters, cudaStream_t st) {
+cudaError_t dispatch(int op, bool pair, const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
   if (op == DP) return launch<DP, B, __nv_bfloat16, true>(p, tm, clusters, st);
-  if (op == FWD) {
-    if (p.f16)
-      return pair ? launch<FWD, B, __half, true>(p, tm, clusters, st) : launch<FWD, B, __half, false>(p, tm, clusters, st);
-    return pair ? launch<FWD, B, __nv_bfloat16, true>(p, tm, clusters, st)
-                : launch<FWD, B, __nv_bfloat16, false>(p, tm, clusters, st);
-  }
-  if (p.f16)
-    return pair ? launch<DX, B, __half, true>(p, tm, clusters, st) : launch<DX, B, __half, false>(p, tm, clusters, st);
-  return pair ? launch<DX, B, __nv_bfloat16, true>(p, tm, clusters, st)
-              : launch<DX, B, __nv_bfloat16, false>(p, tm, clusters, st);
+  if (op == FWD) return pair ? launch_t<FWD, B, true>(p, tm, clusters, st) : launch_t<FWD, B, false>(p, tm, clusters, st);
+  return pair ? launch_t<DX, B, true>(p, tm, clusters, st) : launch_t<DX, B, false>(p, tm, clusters, st);
 }
 
 }  // namespace pg
