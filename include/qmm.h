@@ -429,13 +429,13 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
 qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha, void* out,
                          qmm_dtype out_dtype, int32_t* d_status, void* stream);
 
-/* Workspace bytes of qmm_embedding_backward (-1 when n or rows is outside
- * [0, 2^31 - 1] or cols <= 0). */
+/* Workspace bytes of qmm_embedding_backward (-1 when n is outside [0, 2^31 - 1],
+ * rows outside [0, 2^31 - 2] or cols outside [1, 2^25]). */
 int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
 
 /* Gradient of the lookup in the table's scales and biases, with
- * dW[r, :] = alpha * sum of dy[t, :] over the tokens t with ids[t] = r, taken
- * in token order in fp32.  dy: [n, w->cols] in any float type; dscales,
+ * dW[r, :] = alpha * sum of dy[t, :] over the tokens t with ids[t] = r, in
+ * fp32 and in an order that the ids alone decide.  dy: [n, w->cols] in any float type; dscales,
  * dbiases: [w->rows, w->cols / group_size] in g_dtype (any float type), written
  * whole: rows that no token names get zeros, for n == 0 all of them.  Affine
  * tables; the scales and biases themselves are not read.  A token whose id is

@@ -59,44 +59,306 @@ lookup_kernel(const int32_t* __restrict__ ids, int64_t n, const uint32_t* __rest
   }
 }
 
-// One block per token; the first token of each row sums all of the row's
-// tokens in order.  One thread per 32 codes, groups joined in group order.
-template <int B, typename TD>
-__global__ void __launch_bounds__(256)
-grad_kernel(const TD* __restrict__ dy, const int32_t* __restrict__ ids, int64_t n, const uint32_t* __restrict__ packed,
-            int64_t rows, int64_t cols, int gs, float alpha, void* dscales, void* dbiases, int g_dtype,
-            int32_t* d_status) {
-  const int64_t t0 = blockIdx.x;
-  const int64_t r = ids[t0];
-  if (r < 0 || r >= rows) {
-    if (threadIdx.x == 0) set_status(d_status, QMM_ERR_BAD_TOKEN_ID);
+// ------------------------------------------------------------------ gradient
+// The tokens are sorted by row (stable, so that a row's tokens keep their
+// order and the sums do not depend on timing), and the sorted list is cut into
+// chunks of P tokens.  A chunk sums each of its runs (tokens of one row) over a
+// slab of columns in fp32, multiplies by the row's codes and folds the groups;
+// runs inside a chunk are stored at once, those that cross its ends leave
+// partial group sums that the join adds in list order.  Everything is read
+// once: the bound is dy's bytes (and the output's, zeros included).
+constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kSortCtas = 8;        // one cluster sorts
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kSlabThreads = 128;   // 8 columns each
+constexpr int kSlab = kSlabThreads * 8;
+
+struct SortArgs {
+  const int32_t* ids;
+  int n;
+  int rows;
+  int passes, bits;      // digits of the keys and bits of a digit
+  uint32_t* keys[2];     // ping-pong; pass i writes buffer i & 1
+  uint32_t* perm[2];
+  int32_t* d_status;
+  uint4* zero[2];        // outputs to clear
+  int64_t zero_bytes;    // of each
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t read_rank(const uint32_t* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Cluster 0 sorts by least significant digits, each warp owning a contiguous
+// piece of the list; the other clusters clear the outputs meanwhile.
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs p) {
+  extern __shared__ uint32_t hist[];  // [warp][digit], then a running position
+  __shared__ uint32_t total[kDigits], base[kDigits], wsum[kSortWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x >= kSortCtas) {
+    const int64_t step = (int64_t)(gridDim.x - kSortCtas) * kSortThreads;
+    const int64_t first = (int64_t)(blockIdx.x - kSortCtas) * kSortThreads + tid;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      for (int64_t i = first; i < p.zero_bytes / 16; i += step) p.zero[o][i] = make_uint4(0u, 0u, 0u, 0u);
+      uint16_t* tail = reinterpret_cast<uint16_t*>(p.zero[o]);
+      for (int64_t i = p.zero_bytes / 16 * 8 + first; i < p.zero_bytes / 2; i += step) tail[i] = 0;
+    }
     return;
   }
-  int seen = 0;
-  for (int64_t t = threadIdx.x; t < t0; t += blockDim.x) seen |= ids[t] == r;
-  if (__syncthreads_or(seen)) return;
-  const int64_t G = cols / gs;
-  for (int64_t g = threadIdx.x; g < G; g += blockDim.x) {
-    float ds = 0.0f, db = 0.0f;
-    for (int64_t c = g * gs / 32; c < (g + 1) * gs / 32; ++c) {
-      float a[32];
+  if (p.n == 0) return;  // (the whole cluster)
+  const uint32_t rank = cluster_rank();
+  const int w = (int)rank * kSortWarps + warp, nw = kSortCtas * kSortWarps;
+  const int lo = (int)((int64_t)p.n * w / nw), hi = (int)((int64_t)p.n * (w + 1) / nw);
+  uint32_t* mine = hist + warp * kDigits;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    const uint32_t mask = (1u << p.bits) - 1u;
+    const uint32_t* src_k = p.keys[(pass & 1) ^ 1];
+    const uint32_t* src_p = p.perm[(pass & 1) ^ 1];
+    auto key_at = [&](int i) -> uint32_t {
+      if (pass) return src_k[i];
+      const int32_t id = p.ids[i];
+      return id >= 0 && id < p.rows ? (uint32_t)id : (uint32_t)p.rows;  // bad ids come last
+    };
+    for (int i = tid; i < kSortWarps * kDigits; i += kSortThreads) hist[i] = 0u;
+    __syncthreads();
+    for (int i = lo + lane; i < hi; i += 32) {
+      const uint32_t k = key_at(i);
+      if (pass == 0 && k == (uint32_t)p.rows) set_status(p.d_status, QMM_ERR_BAD_TOKEN_ID);
+      atomicAdd(mine + ((k >> shift) & mask), 1u);
+    }
+    __syncthreads();
+    if (tid < kDigits) {  // counts of this CTA's warps -> exclusive prefixes
+      uint32_t run = 0u;
+#pragma unroll 8
+      for (int j = 0; j < kSortWarps; ++j) {
+        const uint32_t c = hist[j * kDigits + tid];
+        hist[j * kDigits + tid] = run;
+        run += c;
+      }
+      total[tid] = run;
+    }
+    cluster_sync();
+    uint32_t before = 0u, all = 0u;
+    if (tid < kDigits) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) a[i] = 0.0f;
-      for (int64_t t = t0; t < n; ++t)
-        if (ids[t] == r)
-          for (int i = 0; i < 32; ++i) a[i] += to_f32(dy[t * cols + c * 32 + i]);
-      uint32_t wr[B + 1];
-      for (int i = 0; i < B; ++i) wr[i] = packed[r * (cols * B / 32) + c * B + i];
-      wr[B] = 0u;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        ds = fmaf(a[i], (float)stream_code<B>(wr, i), ds);
-        db += a[i];
+      for (int r = 0; r < kSortCtas; ++r) {
+        const uint32_t c = read_rank(total + tid, r);
+        before += r < (int)rank ? c : 0u;
+        all += c;
       }
     }
-    store_as(dscales, g_dtype, r * G + g, alpha * ds);
-    store_as(dbiases, g_dtype, r * G + g, alpha * db);
+    uint32_t incl = all;  // scan over the digits
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    if (tid < kDigits) {
+      uint32_t off = 0u;
+      for (int j = 0; j < warp; ++j) off += wsum[j];
+      base[tid] = off + incl - all + before;
+    }
+    __syncthreads();
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      const uint32_t act = __ballot_sync(0xffffffffu, in);
+      if (in) {
+        const uint32_t k = key_at(i), t = pass ? src_p[i] : (uint32_t)i;
+        const uint32_t d = (k >> shift) & mask;
+        const uint32_t peers = __match_any_sync(act, d);
+        const int r = __popc(peers & ((1u << lane) - 1u));
+        const uint32_t at = base[d] + mine[d] + (uint32_t)r;
+        __syncwarp(act);
+        if (r == 0) mine[d] += (uint32_t)__popc(peers);
+        p.keys[pass & 1][at] = k;
+        p.perm[pass & 1][at] = t;
+      }
+      __syncwarp();
+    }
+    cluster_sync();  // the list is whole, and the totals have been read
   }
+}
+
+struct GradArgs {
+  const void* dy;
+  const uint32_t* keys;  // sorted rows and their tokens
+  const uint32_t* perm;
+  const uint32_t* packed;
+  int n, rows, chunk, chunks;
+  int cols, lgs;
+  float alpha;
+  void* out[2];  // dscales, dbiases
+  int g_dtype;
+  float* part;  // [chunk][first run | last run][scales | biases][groups]
+};
+
+// P list entries x 1024 columns a block; 8 columns a thread.
+template <int B, typename TD>
+__global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, chunk = blockIdx.x;
+  const int e0 = chunk * p.chunk, cnt = min(p.chunk, p.n - e0);
+  // one entry a lane, with the neighbours' keys
+  const uint32_t key = lane < cnt ? p.keys[e0 + lane] : 0xffffffffu;
+  const uint32_t tok = lane < cnt ? p.perm[e0 + lane] : 0u;
+  const uint32_t prev = e0 > 0 ? p.keys[e0 - 1] : 0xffffffffu, next = e0 + cnt < p.n ? p.keys[e0 + cnt] : 0xffffffffu;
+  const int col = blockIdx.y * kSlab + threadIdx.x * 8;
+  const bool live = col < p.cols;
+  const TD* dy = reinterpret_cast<const TD*>(p.dy) + col;
+  const int64_t G = p.cols >> p.lgs;
+  const int lpg = 1 << (p.lgs - 3);  // threads of a group
+  constexpr int U = sizeof(TD) == 4 ? 4 : 8;  // rows requested at a time
+  float acc[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+  int start = 0;
+  for (int i0 = 0; i0 < cnt; i0 += U) {
+    uint4 raw[U][sizeof(TD) / 2];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint32_t t = __shfl_sync(0xffffffffu, tok, (i0 + j) & 31);
+      const uint32_t k = __shfl_sync(0xffffffffu, key, (i0 + j) & 31);
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(TD) / 2; ++h)
+        raw[j][h] = i0 + j < cnt && live && k < (uint32_t)p.rows
+                        ? __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)t * p.cols) + h)
+                        : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j;
+      if (i >= cnt) break;
+      __align__(16) TD v[8];
+      memcpy(v, raw[j], sizeof(v));
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] += to_f32(v[c]);
+      const uint32_t k = __shfl_sync(0xffffffffu, key, i);
+      const uint32_t kn = i + 1 < cnt ? __shfl_sync(0xffffffffu, key, i + 1) : next;
+      if (k == kn && i + 1 < cnt) continue;  // the run goes on
+      if (k < (uint32_t)p.rows) {
+        // the run ends here, or the chunk does
+        float ds = 0.0f, db = 0.0f;
+        if (live) {
+          uint32_t w[3] = {0u, 0u, 0u};
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)k * p.cols + col) / 8 * B;
+          if constexpr (B == 8) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
+            w[0] = q.x;
+            w[1] = q.y;
+          } else if constexpr (B == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+          } else if constexpr (B == 2 || B == 6) {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+            w[0] = __ldg(h);
+            if constexpr (B == 6) {
+              w[0] |= (uint32_t)__ldg(h + 1) << 16;
+              w[1] = __ldg(h + 2);
+            }
+          } else {
+            w[0] = __ldg(src) | ((uint32_t)__ldg(src + 1) << 8) | ((uint32_t)__ldg(src + 2) << 16);
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            ds = fmaf(acc[c], (float)stream_code<B>(w, c), ds);
+            db += acc[c];
+          }
+        }
+        for (int o = 1; o < lpg; o <<= 1) {
+          ds += __shfl_xor_sync(0xffffffffu, ds, o);
+          db += __shfl_xor_sync(0xffffffffu, db, o);
+        }
+        if (live && (threadIdx.x & (lpg - 1)) == 0) {
+          const int g = col >> p.lgs;
+          const bool open = (start == 0 && prev == k) || (i + 1 == cnt && next == k);
+          if (open) {  // a piece of a longer run
+            float* dst = p.part + ((int64_t)chunk * 2 + (start == 0 ? 0 : 1)) * 2 * G;
+            dst[g] = ds;
+            dst[G + g] = db;
+          } else {
+            store_as(p.out[0], p.g_dtype, (int64_t)k * G + g, p.alpha * ds);
+            store_as(p.out[1], p.g_dtype, (int64_t)k * G + g, p.alpha * db);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+      start = i + 1;
+    }
+  }
+}
+
+// The chunk where a run that crosses chunks begins adds its pieces in order.
+__global__ void __launch_bounds__(128) join_kernel(const GradArgs p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int chunk = blockIdx.x, e0 = chunk * p.chunk, last = e0 + p.chunk - 1;
+  if (last + 1 >= p.n) return;
+  const uint32_t k = p.keys[last];
+  if (k >= (uint32_t)p.rows || p.keys[last + 1] != k) return;  // no run goes on
+  const bool whole = p.keys[e0] == k;  // it fills this chunk
+  if (whole && e0 > 0 && p.keys[e0 - 1] == k) return;  // it began earlier
+  const int64_t G = p.cols >> p.lgs;
+  int pieces = 1;  // further chunks of the run
+  while ((int64_t)(chunk + pieces) * p.chunk + p.chunk < p.n && p.keys[(chunk + pieces + 1) * p.chunk] == k) ++pieces;
+  for (int64_t g = threadIdx.x; g < 2 * G; g += blockDim.x) {
+    float sum = p.part[((int64_t)chunk * 2 + (whole ? 0 : 1)) * 2 * G + g];
+#pragma unroll 4
+    for (int c = 1; c <= pieces; ++c) sum += p.part[(int64_t)(chunk + c) * 4 * G + g];
+    store_as(p.out[g >= G], p.g_dtype, (int64_t)k * G + (g >= G ? g - G : g), p.alpha * sum);
+  }
+}
+
+// Tokens of a chunk: up to 32 (one a lane), fewer while that leaves SMs idle.
+static int chunk_of(int64_t n, int64_t cols) {
+  const int64_t slabs = (cols + kSlab - 1) / kSlab;
+  int c = 32;
+  while (c > 4 && (n + c - 1) / c * slabs < 4 * 148) c /= 2;
+  return c;
+}
+
+static int64_t grad_workspace(int64_t n, int64_t cols) {
+  const int64_t chunks = (n + 3) / 4 > 0 ? (n + chunk_of(n, cols) - 1) / chunk_of(n, cols) : 0;
+  // two lists of keys and tokens, and the pieces of two runs a chunk (groups of 32 at most)
+  return 16 + (n + 3) / 4 * 16 * 4 + chunks * 4 * ((cols + 31) / 32) * 4;
+}
+
+template <typename K, typename A>
+static cudaError_t launch_next(K kernel, dim3 grid, int threads, size_t smem, int cluster, const A& args, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
 template <int B, int MODE, typename TS>
@@ -141,24 +403,64 @@ static cudaError_t launch_lookup(const int32_t* ids, int64_t n, const qmm_qweigh
 
 template <typename TD>
 static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha,
-                               void* dscales, void* dbiases, int g_dtype, int32_t* d_status, cudaStream_t st) {
-  const int64_t G = w->cols / w->group_size;
-  const size_t bytes = (size_t)(w->rows * G * qmm_host::dtype_size((qmm_dtype)g_dtype));
-  cudaError_t e = cudaMemsetAsync(dscales, 0, bytes, st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(dbiases, 0, bytes, st);
-  if (e != cudaSuccess || n == 0) return e;
-#define QMM_E(BB)                                                                                                  \
-  grad_kernel<BB, TD><<<(unsigned)n, 256, 0, st>>>((const TD*)dy, ids, n, w->packed, w->rows, w->cols, w->group_size, \
-                                                  alpha, dscales, dbiases, g_dtype, d_status)
-  switch (w->bits) {
-    case 2: QMM_E(2); break;
-    case 3: QMM_E(3); break;
-    case 4: QMM_E(4); break;
-    case 6: QMM_E(6); break;
-    default: QMM_E(8); break;
+                               void* dscales, void* dbiases, int g_dtype, void* workspace, int32_t* d_status,
+                               cudaStream_t st) {
+  const int64_t G = w->cols / w->group_size, n4 = (n + 3) / 4 * 4;
+  uint32_t* ws = static_cast<uint32_t*>(workspace);
+  SortArgs sa{};
+  sa.ids = ids;
+  sa.n = (int)n;
+  sa.rows = (int)w->rows;
+  int bits = 1;
+  while (bits < 32 && (w->rows >> bits) != 0) ++bits;  // keys up to rows
+  sa.passes = (bits + kDigitBits - 1) / kDigitBits;
+  sa.bits = (bits + sa.passes - 1) / sa.passes;
+  for (int i = 0; i < 2; ++i) {
+    sa.keys[i] = ws + (2 * i) * n4;
+    sa.perm[i] = ws + (2 * i + 1) * n4;
+    sa.zero[i] = static_cast<uint4*>(i ? dbiases : dscales);
   }
-#undef QMM_E
-  return cudaGetLastError();
+  sa.d_status = d_status;
+  sa.zero_bytes = w->rows * G * qmm_host::dtype_size((qmm_dtype)g_dtype);
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  constexpr int kSmem = kSortWarps * kDigits * 4;
+  if (!configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = 1;
+  }
+  const int sms = qmm_host::num_sms() / kSortCtas * kSortCtas;
+  cudaError_t e = launch_next(sort_kernel, dim3(sms), kSortThreads, kSmem, kSortCtas, sa, st);
+  if (e != cudaSuccess || n == 0) return e;
+  GradArgs ga{};
+  ga.dy = dy;
+  ga.keys = sa.keys[(sa.passes - 1) & 1];
+  ga.perm = sa.perm[(sa.passes - 1) & 1];
+  ga.packed = w->packed;
+  ga.n = (int)n;
+  ga.rows = (int)w->rows;
+  ga.chunk = chunk_of(n, w->cols);
+  ga.chunks = (int)((n + ga.chunk - 1) / ga.chunk);
+  ga.cols = (int)w->cols;
+  ga.lgs = w->group_size == 32 ? 5 : w->group_size == 64 ? 6 : 7;
+  ga.alpha = alpha;
+  ga.out[0] = dscales;
+  ga.out[1] = dbiases;
+  ga.g_dtype = g_dtype;
+  ga.part = reinterpret_cast<float*>(ws + 4 * n4);
+  const dim3 grid(ga.chunks, (unsigned)((w->cols + kSlab - 1) / kSlab));
+  switch (w->bits) {
+    case 2: e = launch_next(grad_kernel<2, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
+    case 3: e = launch_next(grad_kernel<3, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
+    case 4: e = launch_next(grad_kernel<4, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
+    case 6: e = launch_next(grad_kernel<6, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
+    default: e = launch_next(grad_kernel<8, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
+  }
+  if (e != cudaSuccess || ga.chunks == 1) return e;
+  return launch_next(join_kernel, dim3(ga.chunks - 1), 128, 0, 1, ga, st);
 }
 
 }  // namespace embed
@@ -183,8 +485,10 @@ qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, fl
 }
 
 int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t cols) {
-  if (n < 0 || n > (int64_t)INT32_MAX || rows < 0 || rows > (int64_t)INT32_MAX || cols <= 0) return -1;
-  return 16;
+  if (n < 0 || n > (int64_t)INT32_MAX || rows < 0 || rows >= (int64_t)INT32_MAX || cols <= 0 ||
+      cols > (1 << 25))
+    return -1;
+  return qmm::embed::grad_workspace(n, cols);
 }
 
 qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int32_t* ids, int64_t n,
@@ -205,11 +509,14 @@ qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int3
   if (s != QMM_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
   if (dy_dtype == QMM_F32)
-    return launch_status(qmm::embed::launch_grad<float>(dy, ids, n, w, alpha, dscales, dbiases, g_dtype, d_status, st));
+    return launch_status(qmm::embed::launch_grad<float>(dy, ids, n, w, alpha, dscales, dbiases, g_dtype, workspace,
+                                                        d_status, st));
   if (dy_dtype == QMM_BF16)
     return launch_status(
-        qmm::embed::launch_grad<__nv_bfloat16>(dy, ids, n, w, alpha, dscales, dbiases, g_dtype, d_status, st));
-  return launch_status(qmm::embed::launch_grad<__half>(dy, ids, n, w, alpha, dscales, dbiases, g_dtype, d_status, st));
+        qmm::embed::launch_grad<__nv_bfloat16>(dy, ids, n, w, alpha, dscales, dbiases, g_dtype, workspace,
+                                                        d_status, st));
+  return launch_status(qmm::embed::launch_grad<__half>(dy, ids, n, w, alpha, dscales, dbiases, g_dtype, workspace,
+                                                        d_status, st));
 }
 
 }  // extern "C"
