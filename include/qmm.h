@@ -413,8 +413,8 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
  * the same bits.
  *
  * Workspaces are device memory of the caller, 16-byte aligned, of at least
- * the bytes that the matching ..._workspace_bytes call gives; a call writes
- * what it reads there, so the contents need no preparation.  Two calls that
+ * the bytes that the matching ..._workspace_bytes call gives (0: NULL will do);
+ * a call writes what it reads there, so the contents need no preparation.  Two calls that
  * may overlap on the GPU (two streams, two captured graphs) need two.
  * ------------------------------------------------------------------------ */
 
@@ -451,7 +451,7 @@ qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int3
 
 /* Workspace bytes of qmm_gate_up_silu (-1 for a size outside [0, 2^31 - 1] or
  * M * F or F * K past 2^57): room for both dequantized weights for many
- * tokens, 16 bytes otherwise. */
+ * tokens, 0 otherwise. */
 int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F);
 
 /* The gated projection: h[M, F] = SiLU(x . dequant(gate)^T) * (x .

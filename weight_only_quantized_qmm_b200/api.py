@@ -591,53 +591,69 @@ def qmm_moe_gemm_id_noalloc(a: torch.Tensor, ids: torch.Tensor, batch: int, top_
 
 
 # ------------------------------------------------------------------ embedding, gated block, gradients
-def _weights_here(call: str, tensors: dict, weights: dict):
-    """The C structs of `weights` (name -> QWeight) once every tensor of
-    `tensors` (name -> tensor or None) and every weight is on the current
-    device; ValueError otherwise."""
-    preps = []
-    for name, w in weights.items():
+def _structs(call: str, names, tensors, weights):
+    """(device, C structs of `weights`) once every tensor (or None) of `tensors`
+    and every (name, QWeight) of `weights` is on the current device;
+    ValueError otherwise."""
+    dev = tensors[0].get_device()  # -1: host memory
+    here = dev >= 0
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            here = False
+    cs = []
+    for name, w in weights:
         try:
-            preps.append(w.prepared())
+            d, c = w.prepared()
         except ValueError as e:
             raise ValueError(f"{call}: {name}: {e}") from None
-    devs = {t.get_device() for t in tensors.values() if t is not None}
-    devs.update(d for d, _ in preps)
-    if len(devs) != 1 or None in devs or min(devs) < 0 or devs.pop() != torch.cuda.current_device():
+        if d != dev:
+            here = False
+        cs.append(c)
+    if not here or dev != torch.cuda.current_device():
         # the slow checks name the tensor that is elsewhere
-        _on_device(**tensors)
-        for name, w in weights.items():
+        _on_device(**dict(zip(names, tensors)))
+        for name, w in weights:
             _on_device(**{f"{name}.{k}": t for k, t in w.validate().items()})
         raise ValueError(f"{call}: the weights are not all on the current device")
-    return [c for _, c in preps]
+    return dev, cs
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
+def _handle(stream, dev: int) -> int:
+    return int(stream.cuda_stream) if stream is not None else int(torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """An output or workspace of a call on `stream`: memory of that stream, so
     that nothing still running elsewhere uses it, kept until the current
     stream is done with it too."""
-    if stream is None or torch.device(device).type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
 def _dense(t: torch.Tensor, stream) -> torch.Tensor:
     """`t`, or its contiguous copy made on the call's stream."""
-    if t.is_contiguous() or stream is None or not t.is_cuda:
+    if t.is_contiguous():
+        return t
+    if stream is None or not t.is_cuda:
         return t.contiguous()
     t.record_stream(stream)
     with torch.cuda.stream(stream):
         return t.contiguous()
 
 
-def _exactly(t, what: str, shape, dtypes, device, stream) -> torch.Tensor:
+def _exactly(t, what: str, shape, dtypes, like: torch.Tensor, stream) -> torch.Tensor:
     """`t` checked to be a contiguous tensor of `shape` and one of `dtypes`, or
     a new one of the first dtype."""
     if t is None:
-        return _new(shape, dtypes[0], device, stream)
+        return _new(shape, dtypes[0], like, stream)
     n = 1
     for d in shape:
         n *= d
@@ -647,22 +663,27 @@ def _exactly(t, what: str, shape, dtypes, device, stream) -> torch.Tensor:
     return t
 
 
-def _workspace(call: str, workspace, nbytes: int, device, stream) -> torch.Tensor:
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(call: str, *sizes: int) -> int:
+    nbytes = int(getattr(_lib.load(), call + "_workspace_bytes")(*sizes))
     if nbytes < 0:
         check(call, _lib.QMM_ERR_INVALID_ARG)
+    return nbytes
+
+
+def _workspace(call: str, workspace, sizes, like: torch.Tensor, stream):
+    """(workspace or None, its bytes)"""
+    need = _workspace_bytes(call, *sizes)
     if workspace is None:
-        return _new((nbytes,), torch.uint8, device, stream)
-    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError(f"{call}: workspace must be contiguous and hold at least {nbytes} bytes")
-    return workspace
-
-
-def _nbytes(t: torch.Tensor) -> int:
-    return t.numel() * t.element_size()
+        return (None if need == 0 else _new((need,), torch.uint8, like, stream)), need
+    have = workspace.numel() * workspace.element_size()
+    if not workspace.is_contiguous() or have < need:
+        raise ValueError(f"{call}: workspace must be contiguous and hold at least {need} bytes")
+    return workspace, have
 
 
 def _rows_of(t: torch.Tensor, what: str, cols: int, lead, dtype, stream) -> torch.Tensor:
-    """[..., cols] with leading dimensions `lead` as contiguous [rows, cols]."""
+    """[..., cols] with leading dimensions `lead`, contiguous."""
     if t.dim() < 1 or t.shape[-1] != cols or t.shape[:-1] != lead:
         raise ValueError(f"qmm: {what} has shape {tuple(t.shape)}, expected {(*lead, cols)}")
     if t.dtype != dtype:
@@ -677,15 +698,17 @@ def qmm_embedding(ids: torch.Tensor, qw: QWeight, alpha: float = 1.0, y_dtype: t
     QMM_ERR_BAD_TOKEN_ID in d_status.  y_dtype: the scales' dtype by default
     (float32 for a microscaled table)."""
     n = ids.numel()
-    _need(ids, "ids", n, (torch.int32,))
+    _need(ids, "ids", n, _PACKED)
     if d_status is not None:
-        _need(d_status, "d_status", 1, (torch.int32,))
-    if y_dtype is None:
-        y_dtype = qw.scales.dtype if qw.mode == QMM_MODE_AFFINE else torch.float32
-    out = _exactly(out, "out", (*ids.shape, qw.cols), _FLOAT if out is not None else (y_dtype,), ids.device, stream)
-    (c,) = _weights_here("qmm_embedding", {"ids": ids, "out": out, "d_status": d_status}, {"table": qw})
-    rc = _lib.load().qmm_embedding(_ptr(ids), n, ctypes.byref(c), float(alpha), _ptr(out), dtype_code(out.dtype),
-                                   _ptr(d_status), _stream(stream))
+        _need(d_status, "d_status", 1, _PACKED)
+    if out is None:
+        dt = y_dtype or (qw.scales.dtype if qw.mode == QMM_MODE_AFFINE else torch.float32)
+        out = _new((*ids.shape, qw.cols), dt, ids, stream)
+    else:
+        out = _exactly(out, "out", (*ids.shape, qw.cols), _FLOAT, ids, stream)
+    dev, (c,) = _structs("qmm_embedding", ("ids", "out", "d_status"), (ids, out, d_status), (("table", qw),))
+    rc = _lib.load().qmm_embedding(ids.data_ptr(), n, ctypes.byref(c), float(alpha), out.data_ptr(),
+                                   dtype_code(out.dtype), _addr(d_status), _handle(stream, dev))
     check("qmm_embedding", rc)
     return out
 
@@ -696,25 +719,22 @@ def qmm_embedding_backward(dy: torch.Tensor, ids: torch.Tensor, qw: QWeight, alp
     """(dscales, dbiases), [rows, groups] each, of the lookup's table from
     dy [*ids.shape, cols]; g_dtype is the scales' dtype by default."""
     n = ids.numel()
-    _need(ids, "ids", n, (torch.int32,))
+    _need(ids, "ids", n, _PACKED)
     if d_status is not None:
-        _need(d_status, "d_status", 1, (torch.int32,))
+        _need(d_status, "d_status", 1, _PACKED)
     if qw.mode != QMM_MODE_AFFINE:
         check("qmm_embedding_backward", _lib.QMM_ERR_UNSUPPORTED)
     dy = _rows_of(dy, "dy", qw.cols, ids.shape, dy.dtype, stream)
-    _need(dy, "dy", n * qw.cols, _FLOAT)
-    G = _groups(qw.cols, qw.group_size)
+    shape = (qw.rows, _groups(qw.cols, qw.group_size))
     g_dtype = g_dtype or (dscales if dscales is not None else qw.scales).dtype
-    dscales = _exactly(dscales, "dscales", (qw.rows, G), (g_dtype,), dy.device, stream)
-    dbiases = _exactly(dbiases, "dbiases", (qw.rows, G), (g_dtype,), dy.device, stream)
-    L = _lib.load()
-    ws = _workspace("qmm_embedding_backward", workspace,
-                    L.qmm_embedding_backward_workspace_bytes(n, qw.rows, qw.cols), dy.device, stream)
-    (c,) = _weights_here("qmm_embedding_backward", {"dy": dy, "ids": ids, "dscales": dscales, "dbiases": dbiases,
-                                                    "workspace": ws, "d_status": d_status}, {"table": qw})
-    rc = L.qmm_embedding_backward(_ptr(dy), dtype_code(dy.dtype), _ptr(ids), n, ctypes.byref(c), float(alpha),
-                                  _ptr(dscales), _ptr(dbiases), dtype_code(g_dtype), _ptr(ws), _nbytes(ws),
-                                  _ptr(d_status), _stream(stream))
+    dscales = _exactly(dscales, "dscales", shape, (g_dtype,), dy, stream)
+    dbiases = _exactly(dbiases, "dbiases", shape, (g_dtype,), dy, stream)
+    ws, nbytes = _workspace("qmm_embedding_backward", workspace, (n, qw.rows, qw.cols), dy, stream)
+    dev, (c,) = _structs("qmm_embedding_backward", ("dy", "ids", "dscales", "dbiases", "workspace", "d_status"),
+                         (dy, ids, dscales, dbiases, ws, d_status), (("table", qw),))
+    rc = _lib.load().qmm_embedding_backward(
+        dy.data_ptr(), dtype_code(dy.dtype), ids.data_ptr(), n, ctypes.byref(c), float(alpha), dscales.data_ptr(),
+        dbiases.data_ptr(), dtype_code(g_dtype), _addr(ws), nbytes, _addr(d_status), _handle(stream, dev))
     check("qmm_embedding_backward", rc)
     return dscales, dbiases
 
@@ -724,20 +744,23 @@ def qmm_gate_up_silu(x: torch.Tensor, gate: QWeight, up: QWeight, y_dtype: torch
     """h = SiLU(x . dequant(gate)^T) * (x . dequant(up)^T); x [..., K], h [..., F].
     With save (or g_pre and u_pre given) returns (h, g, u), the projections
     in x's dtype that qmm_gate_up_silu_backward reads."""
-    lead, K, F = x.shape[:-1], x.shape[-1], gate.rows
+    K, F = x.shape[-1], gate.rows
+    shape = (*x.shape[:-1], F)
     x2 = _dense(x, stream)
     M = x2.numel() // K if K else 0
-    _need(x2, "x", M * K, _FLOAT)
-    out = _exactly(out, "out", (*lead, F), _FLOAT if out is not None else (y_dtype or x.dtype,), x2.device, stream)
+    if out is None:
+        out = _new(shape, y_dtype or x.dtype, x2, stream)
+    else:
+        out = _exactly(out, "out", shape, _FLOAT, x2, stream)
     if save or g_pre is not None or u_pre is not None:
-        g_pre = _exactly(g_pre, "g_pre", (*lead, F), (x.dtype,), x2.device, stream)
-        u_pre = _exactly(u_pre, "u_pre", (*lead, F), (x.dtype,), x2.device, stream)
-    L = _lib.load()
-    ws = _workspace("qmm_gate_up_silu", workspace, L.qmm_gate_up_silu_workspace_bytes(M, K, F), x2.device, stream)
-    cg, cu = _weights_here("qmm_gate_up_silu", {"x": x2, "out": out, "g_pre": g_pre, "u_pre": u_pre, "workspace": ws},
-                           {"gate": gate, "up": up})
-    rc = L.qmm_gate_up_silu(_ptr(x2), dtype_code(x2.dtype), M, K, ctypes.byref(cg), ctypes.byref(cu), _ptr(out),
-                            dtype_code(out.dtype), _ptr(g_pre), _ptr(u_pre), _ptr(ws), _nbytes(ws), _stream(stream))
+        g_pre = _exactly(g_pre, "g_pre", shape, (x.dtype,), x2, stream)
+        u_pre = _exactly(u_pre, "u_pre", shape, (x.dtype,), x2, stream)
+    ws, nbytes = _workspace("qmm_gate_up_silu", workspace, (M, K, F), x2, stream)
+    dev, (cg, cu) = _structs("qmm_gate_up_silu", ("x", "out", "g_pre", "u_pre", "workspace"),
+                             (x2, out, g_pre, u_pre, ws), (("gate", gate), ("up", up)))
+    rc = _lib.load().qmm_gate_up_silu(
+        x2.data_ptr(), dtype_code(x2.dtype), M, K, ctypes.byref(cg), ctypes.byref(cu), out.data_ptr(),
+        dtype_code(out.dtype), _addr(g_pre), _addr(u_pre), _addr(ws), nbytes, _handle(stream, dev))
     check("qmm_gate_up_silu", rc)
     return out if g_pre is None else (out, g_pre, u_pre)
 
@@ -748,28 +771,26 @@ def qmm_matmul_backward(dy: torch.Tensor, x: torch.Tensor, qw: QWeight, need_dx:
     """Gradients of qmm_matmul(x, qw): (dx, dscales, dbiases), None for what is
     not asked for; dy [..., N], x [..., K], g_dtype x's dtype (default) or
     float32."""
-    lead, K, N = x.shape[:-1], x.shape[-1], qw.rows
+    lead, K, N, dt = x.shape[:-1], x.shape[-1], qw.rows, x.dtype
     if K != qw.cols:
         check("qmm_matmul_backward", _lib.QMM_ERR_INVALID_ARG)
-    x2 = _rows_of(x, "x", K, lead, x.dtype, stream)
-    dy2 = _rows_of(dy, "dy", N, lead, x.dtype, stream)
-    _need(x2, "x", x2.numel(), _FLOAT)
+    x2 = _dense(x, stream)
+    dy2 = _rows_of(dy, "dy", N, lead, dt, stream)
     M = x2.numel() // K
-    g_dtype = g_dtype or (dscales.dtype if dscales is not None else x.dtype)
-    dx = _exactly(dx, "dx", x.shape, (x.dtype,), x2.device, stream) if need_dx else None
+    g_dtype = g_dtype or (dscales.dtype if dscales is not None else dt)
+    dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream) if need_dx else None
     if need_params:
-        G = _groups(K, qw.group_size)
-        dscales = _exactly(dscales, "dscales", (N, G), (g_dtype,), x2.device, stream)
-        dbiases = _exactly(dbiases, "dbiases", (N, G), (g_dtype,), x2.device, stream)
+        shape = (N, _groups(K, qw.group_size))
+        dscales = _exactly(dscales, "dscales", shape, (g_dtype,), x2, stream)
+        dbiases = _exactly(dbiases, "dbiases", shape, (g_dtype,), x2, stream)
     else:
         dscales = dbiases = None
-    L = _lib.load()
-    ws = _workspace("qmm_matmul_backward", workspace, L.qmm_matmul_backward_workspace_bytes(M, K, N), x2.device, stream)
-    (c,) = _weights_here("qmm_matmul_backward", {"dy": dy2, "x": x2, "dx": dx, "dscales": dscales, "dbiases": dbiases,
-                                                 "workspace": ws}, {"w": qw})
-    rc = L.qmm_matmul_backward(_ptr(dy2), _ptr(x2), dtype_code(x2.dtype), M, K, ctypes.byref(c), _ptr(dx),
-                               _ptr(dscales), _ptr(dbiases), dtype_code(g_dtype), _ptr(ws), _nbytes(ws),
-                               _stream(stream))
+    ws, nbytes = _workspace("qmm_matmul_backward", workspace, (M, K, N), x2, stream)
+    dev, (c,) = _structs("qmm_matmul_backward", ("dy", "x", "dx", "dscales", "dbiases", "workspace"),
+                         (dy2, x2, dx, dscales, dbiases, ws), (("w", qw),))
+    rc = _lib.load().qmm_matmul_backward(
+        dy2.data_ptr(), x2.data_ptr(), dtype_code(dt), M, K, ctypes.byref(c), _addr(dx), _addr(dscales),
+        _addr(dbiases), dtype_code(g_dtype), _addr(ws), nbytes, _handle(stream, dev))
     check("qmm_matmul_backward", rc)
     return dx, dscales, dbiases
 
@@ -781,33 +802,33 @@ def qmm_gate_up_silu_backward(dh: torch.Tensor, x: torch.Tensor, g_pre: torch.Te
     """Gradients of qmm_gate_up_silu from its saved g_pre and u_pre: (dx,
     (dgate_scales, dgate_biases), (dup_scales, dup_biases)), None for what is
     not asked for; g_dtype is x's dtype (default) or float32."""
-    lead, K, F = x.shape[:-1], x.shape[-1], gate.rows
+    lead, K, F, dt = x.shape[:-1], x.shape[-1], gate.rows, x.dtype
     if K != gate.cols or K != up.cols or F != up.rows:
         check("qmm_gate_up_silu_backward", _lib.QMM_ERR_INVALID_ARG)
-    x2 = _rows_of(x, "x", K, lead, x.dtype, stream)
-    dh2, g2, u2 = (_rows_of(t, n, F, lead, x.dtype, stream)
-                    for t, n in ((dh, "dh"), (g_pre, "g_pre"), (u_pre, "u_pre")))
-    _need(x2, "x", x2.numel(), _FLOAT)
+    x2 = _dense(x, stream)
+    dh2 = _rows_of(dh, "dh", F, lead, dt, stream)
+    g2 = _rows_of(g_pre, "g_pre", F, lead, dt, stream)
+    u2 = _rows_of(u_pre, "u_pre", F, lead, dt, stream)
     M = x2.numel() // K
-    g_dtype = g_dtype or (dgate[0].dtype if dgate is not None else x.dtype)
-    dx = _exactly(dx, "dx", x.shape, (x.dtype,), x2.device, stream) if need_dx else None
-    grads = [None] * 4
+    g_dtype = g_dtype or (dgate[0].dtype if dgate is not None else dt)
+    dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream) if need_dx else None
+    gs = gz = us = uz = None
     if need_params:
-        G = _groups(K, gate.group_size)
-        given = [*(dgate or (None, None)), *(dup or (None, None))]
-        names = ("dgate_scales", "dgate_biases", "dup_scales", "dup_biases")
-        grads = [_exactly(t, n, (F, G), (g_dtype,), x2.device, stream) for t, n in zip(given, names)]
-    L = _lib.load()
-    ws = _workspace("qmm_gate_up_silu_backward", workspace, L.qmm_gate_up_silu_backward_workspace_bytes(M, K, F),
-                    x2.device, stream)
-    cg, cu = _weights_here("qmm_gate_up_silu_backward",
-                           {"dh": dh2, "x": x2, "g_pre": g2, "u_pre": u2, "dx": dx, "dgate_scales": grads[0],
-                            "dgate_biases": grads[1], "dup_scales": grads[2], "dup_biases": grads[3],
-                            "workspace": ws}, {"gate": gate, "up": up})
-    rc = L.qmm_gate_up_silu_backward(_ptr(dh2), _ptr(x2), _ptr(g2), _ptr(u2), dtype_code(x2.dtype), M, K,
-                                     ctypes.byref(cg), ctypes.byref(cu), _ptr(dx), *(_ptr(t) for t in grads),
-                                     dtype_code(g_dtype), _ptr(ws), _nbytes(ws), _stream(stream))
+        shape = (F, _groups(K, gate.group_size))
+        gs, gz = dgate or (None, None)
+        us, uz = dup or (None, None)
+        gs = _exactly(gs, "dgate_scales", shape, (g_dtype,), x2, stream)
+        gz = _exactly(gz, "dgate_biases", shape, (g_dtype,), x2, stream)
+        us = _exactly(us, "dup_scales", shape, (g_dtype,), x2, stream)
+        uz = _exactly(uz, "dup_biases", shape, (g_dtype,), x2, stream)
+    ws, nbytes = _workspace("qmm_gate_up_silu_backward", workspace, (M, K, F), x2, stream)
+    dev, (cg, cu) = _structs(
+        "qmm_gate_up_silu_backward",
+        ("dh", "x", "g_pre", "u_pre", "dx", "dgate_scales", "dgate_biases", "dup_scales", "dup_biases", "workspace"),
+        (dh2, x2, g2, u2, dx, gs, gz, us, uz, ws), (("gate", gate), ("up", up)))
+    rc = _lib.load().qmm_gate_up_silu_backward(
+        dh2.data_ptr(), x2.data_ptr(), g2.data_ptr(), u2.data_ptr(), dtype_code(dt), M, K, ctypes.byref(cg),
+        ctypes.byref(cu), _addr(dx), _addr(gs), _addr(gz), _addr(us), _addr(uz), dtype_code(g_dtype), _addr(ws),
+        nbytes, _handle(stream, dev))
     check("qmm_gate_up_silu_backward", rc)
-    if not need_params:
-        return dx, None, None
-    return dx, (grads[0], grads[1]), (grads[2], grads[3])
+    return (dx, (gs, gz), (us, uz)) if need_params else (dx, None, None)

@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "pair_gemm.cuh"
+#include "qgemv.cuh"
 
 namespace qmm {
 namespace pg {
@@ -251,7 +252,7 @@ extern "C" {
 
 int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F) {
   if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F)) return -1;
-  return 16 + qmm::ffn::dense_bytes(M, K, F, 2);
+  return qmm::ffn::dense_bytes(M, K, F, 2);
 }
 
 qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
@@ -264,10 +265,16 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
   const int64_t need = qmm_gate_up_silu_workspace_bytes(M, K, gate->rows);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M == 0 || gate->rows == 0) return QMM_OK;
-  if (!aligned16(workspace) || !aligned16(x) || !aligned16(h) || (g_pre && (!aligned16(g_pre) || !aligned16(u_pre)))) return QMM_ERR_ALIGNMENT;
+  if (need > 0 && !aligned16(workspace)) return QMM_ERR_ALIGNMENT;
+  if (!aligned16(x) || !aligned16(h) || (g_pre && (!aligned16(g_pre) || !aligned16(u_pre)))) return QMM_ERR_ALIGNMENT;
   s = qmm_device_check();
   if (s != QMM_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
+  if (M <= 16) {  // few tokens: the streaming kernels, both matrices in one pass
+    const qmm::QgemvParams p = qmm::make_gated_params(x, x_dtype, M, K, gate, up, h, h_dtype, g_pre, u_pre);
+    const cudaError_t e = qmm::launch_qgemv(p, gate->bits, gate->group_size, x_dtype, true, st);
+    if (e != cudaErrorInvalidValue) return launch_status(e);
+  }
   return launch_status(qmm::ffn::forward(x, x_dtype, M, K, gate, up, h, h_dtype, g_pre, u_pre,
                                          qmm::ffn::dense_first(M) ? workspace : nullptr, st));
 }
@@ -275,7 +282,7 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
 int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (!i32(M) || !i32(K) || !i32(N) || !fits(M, K, N)) return -1;
   // rows of dy that do not start on 16 bytes are copied to ones that do
-  return 16 + qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) + qmm::ffn::dense_bytes(M, K, N, 1);
+  return qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) + qmm::ffn::dense_bytes(M, K, N, 1);
 }
 
 qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype, int64_t M, int64_t K,
@@ -288,7 +295,8 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
   const int64_t need = qmm_matmul_backward_workspace_bytes(M, K, w->rows);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M > 0 && w->rows > 0 && (!aligned16(dy) || !aligned16(x))) return QMM_ERR_ALIGNMENT;
-  if ((dx && !aligned16(dx)) || (dscales && (!aligned16(dscales) || !aligned16(dbiases))) || !aligned16(workspace))
+  if ((dx && !aligned16(dx)) || (dscales && (!aligned16(dscales) || !aligned16(dbiases))) ||
+      (need > 0 && !aligned16(workspace)))
     return QMM_ERR_ALIGNMENT;
   s = qmm_device_check();
   if (s != QMM_OK) return s;
@@ -308,7 +316,7 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
 
 int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F) {
   if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F)) return -1;
-  return 16 + qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) + qmm::ffn::dense_bytes(M, K, F, 2);  // dg and du first
+  return qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) + qmm::ffn::dense_bytes(M, K, F, 2);  // dg and du first
 }
 
 qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* g_pre, const void* u_pre,
@@ -328,7 +336,7 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M > 0 && F > 0 && (!aligned16(dh) || !aligned16(x) || !aligned16(g_pre) || !aligned16(u_pre)))
     return QMM_ERR_ALIGNMENT;
-  if ((dx && !aligned16(dx)) || !aligned16(workspace)) return QMM_ERR_ALIGNMENT;
+  if ((dx && !aligned16(dx)) || (need > 0 && !aligned16(workspace))) return QMM_ERR_ALIGNMENT;
   for (int i = 0; i < 4; ++i)
     if (grads[i] && !aligned16(grads[i])) return QMM_ERR_ALIGNMENT;
   s = qmm_device_check();

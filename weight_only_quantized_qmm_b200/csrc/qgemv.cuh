@@ -23,6 +23,8 @@ struct QgemvParams {
   void* out;
   int out_dtype;
   int64_t out_ld;
+  void* pre[2];        // fused form: where the two projections go (rows of out_ld), or nullptr
+  int pre_dtype;
   int32_t* d_status;
   int tok_cap;         // tokens per pass (<= 8*MT)
   int kchunk;          // groups staged per K chunk
@@ -63,6 +65,20 @@ inline QgemvParams make_dense_params(const void* x, int64_t M, int64_t K, const 
   p.out_ld = ldy;
   p.d_status = nullptr;
   p.use_tma = 1;
+  return p;
+}
+
+// gate and up of one dense layer: h = SiLU(x . gate^T) * (x . up^T), and the
+// two projections in x's dtype when g_pre is given
+inline QgemvParams make_gated_params(const void* x, int x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
+                                     const qmm_qweight* up, void* h, int h_dtype, void* g_pre, void* u_pre) {
+  QgemvParams p = make_dense_params(x, M, K, gate, h, gate->rows, h_dtype);
+  p.packed[1] = up->packed;
+  p.scales[1] = up->scales;
+  p.biases[1] = up->biases;
+  p.pre[0] = g_pre;
+  p.pre[1] = u_pre;
+  p.pre_dtype = x_dtype;
   return p;
 }
 

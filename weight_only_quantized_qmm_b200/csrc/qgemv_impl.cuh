@@ -388,7 +388,13 @@ __device__ __forceinline__ void reduce_store(const QgemvParams& p, const float* 
       if (DUAL) y1 += pp[1];
     }
     float yv = y0;
-    if (DUAL) yv = y0 / (1.0f + expf(-y0)) * y1;
+    if (DUAL) {
+      yv = y0 / (1.0f + expf(-y0)) * y1;
+      if (p.pre[0]) {
+        store_as(p.pre[0], p.pre_dtype, (int64_t)pairs[tk] * p.out_ld + row, y0);
+        store_as(p.pre[1], p.pre_dtype, (int64_t)pairs[tk] * p.out_ld + row, y1);
+      }
+    }
     store_as(p.out, p.out_dtype, (int64_t)pairs[tk] * p.out_ld + row, yv);
   }
 }

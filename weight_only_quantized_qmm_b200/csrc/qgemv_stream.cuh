@@ -537,6 +537,14 @@ __device__ __forceinline__ void stage_x(const QgemvParams& q, const int* pairs, 
     if (idx % TOKP >= np) rec[idx] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 
+// the gated block's two projections, where they are asked for
+__device__ __forceinline__ void store_pre(const QgemvParams& q, int64_t at, float g, float u) {
+  if (q.pre[0]) {
+    store_as(q.pre[0], q.pre_dtype, at, g);
+    store_as(q.pre[1], q.pre_dtype, at, u);
+  }
+}
+
 // PT (8-bit codes only): per-tensor dynamic-range int8 ("mlex 0.1.3
 // src/quant.rs"): the codes are int8 q, u = q + 128 is the code the lanes
 // decode, and one scale fl((out_max - out_min) / 255) with bias out_min
@@ -606,6 +614,11 @@ qgemv_stream_kernel(const Params p, const __grid_constant__ CUtensorMap tmc0, co
       if constexpr (!PT) {
         tma_prefetch_2d(&tms0, ku * GPU, y);
         tma_prefetch_2d(&tmb0, ku * GPU, y);
+      }
+      if constexpr (NS == 2) {
+        tma_prefetch_3d(&tmc1, 0, y, ku * C::Z);
+        tma_prefetch_2d(&tms1, ku * GPU, y);
+        tma_prefetch_2d(&tmb1, ku * GPU, y);
       }
     }
   }
@@ -763,7 +776,10 @@ qgemv_stream_kernel(const Params p, const __grid_constant__ CUtensorMap tmc0, co
             }
             const float v = NS == 2 ? y[0] / (1.0f + expf(-y[0])) * y[NS - 1] : y[0];
             const int64_t row = (int64_t)w.rt * C::ROWS + rt * 16 + rr;
-            if (row < q.n_rows) store_as(q.out, q.out_dtype, (int64_t)pairs[0] * q.out_ld + row, v);
+            if (row < q.n_rows) {
+              store_as(q.out, q.out_dtype, (int64_t)pairs[0] * q.out_ld + row, v);
+              if constexpr (NS == 2 && !MOE) store_pre(q, (int64_t)pairs[0] * q.out_ld + row, y[0], y[NS - 1]);
+            }
           }
         } else {
           // partials: [entry][consumer][matrix][token tile][lane] float4 (the mma C fragment)
@@ -785,7 +801,10 @@ qgemv_stream_kernel(const Params p, const __grid_constant__ CUtensorMap tmc0, co
             }
             const float v = NS == 2 ? y[0] / (1.0f + expf(-y[0])) * y[NS - 1] : y[0];
             const int64_t row = (int64_t)w.rt * C::ROWS + rt * 16 + r;
-            if (row < q.n_rows) store_as(q.out, q.out_dtype, (int64_t)pairs[m] * q.out_ld + row, v);
+            if (row < q.n_rows) {
+              store_as(q.out, q.out_dtype, (int64_t)pairs[m] * q.out_ld + row, v);
+              if constexpr (NS == 2 && !MOE) store_pre(q, (int64_t)pairs[m] * q.out_ld + row, y[0], y[NS - 1]);
+            }
           }
         }
       }
@@ -1188,6 +1207,22 @@ cudaError_t launch_stream(const QgemvParams& q, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, p, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5]);
 }
 
+// A dense call of nine to sixteen tokens whose x rows do not fit beside the
+// ring, as two of up to eight tokens (tokens 8.. read x and write their outputs
+// eight rows further on).
+template <typename T>
+struct TokenHalves {
+  QgemvParams lo, hi;
+  explicit TokenHalves(const QgemvParams& q) : lo(q), hi(q) {
+    lo.n_pairs = 8;
+    hi.n_pairs = q.n_pairs - 8;
+    hi.a = reinterpret_cast<const T*>(q.a) + 8 * q.K;
+    hi.out = reinterpret_cast<uint8_t*>(q.out) + 8 * q.out_ld * (q.out_dtype == QMM_F32 ? 4 : 2);
+    for (int i = 0; i < 2; ++i)
+      if (q.pre[i]) hi.pre[i] = reinterpret_cast<T*>(q.pre[i]) + 8 * q.out_ld;
+  }
+};
+
 // Instantiation for one (bits, group size, dtype): the unit width and mode.
 // Dense calls: one token -> mode 0, up to 8 -> 1, up to 16 -> 2.  MoE calls:
 // one activation row per expert is the common case for a single token, so
@@ -1199,6 +1234,15 @@ cudaError_t try_stream_t(const QgemvParams& q, int mt, bool dual, cudaStream_t s
     constexpr int WPG = L::kWordsPerGroup;
     constexpr int UB = WPG > 16 ? 16 : 32;   // base unit (at most 16 slices)
     constexpr int UW = WPG <= 8 ? 64 : UB;   // wide unit: 4 groups per consumer
+    if (dual && !q.ids) {  // gate and up of one dense layer
+      if (q.n_pairs == 1) return launch_stream<BITS, GS, T, 0, UB, 2, false>(q, st);
+      if (mt == 1) return launch_stream<BITS, GS, T, 1, UB, 2, false>(q, st);
+      const cudaError_t e2 = launch_stream<BITS, GS, T, 2, UB, 2, false>(q, st);
+      if (e2 != cudaErrorNotSupported) return e2;
+      const TokenHalves<T> h(q);
+      const cudaError_t e = launch_stream<BITS, GS, T, 1, UB, 2, false>(h.lo, st);
+      return e != cudaSuccess ? e : launch_stream<BITS, GS, T, 1, UB, 2, false>(h.hi, st);
+    }
     if (dual) {
       if (q.n_pairs <= 8) return launch_stream<BITS, GS, T, 0, UB, 2, true>(q, st);
       return launch_stream<BITS, GS, T, 1, UB, 2, true>(q, st);
@@ -1231,17 +1275,12 @@ cudaError_t try_stream_t(const QgemvParams& q, int mt, bool dual, cudaStream_t s
       return wide ? launch_stream<BITS, GS, T, 1, UW, 1, false>(q, st) : launch_stream<BITS, GS, T, 1, UB, 1, false>(q, st);
     const cudaError_t e2 = launch_stream<BITS, GS, T, 2, UB, 1, false>(q, st);
     if (e2 != cudaErrorNotSupported || q.n_pairs <= 8 || q.amode != 0) return e2;
-    // sixteen tokens' x rows do not fit beside the ring: two passes of up to
-    // eight tokens each (tokens 8.. read x and write y eight rows further on)
-    QgemvParams lo = q, hi = q;
-    lo.n_pairs = 8;
-    hi.n_pairs = q.n_pairs - 8;
-    hi.a = reinterpret_cast<const T*>(q.a) + 8 * q.K;
-    hi.out = reinterpret_cast<uint8_t*>(q.out) + 8 * q.out_ld * (q.out_dtype == QMM_F32 ? 4 : 2);
-    const cudaError_t e = wide ? launch_stream<BITS, GS, T, 1, UW, 1, false>(lo, st)
-                               : launch_stream<BITS, GS, T, 1, UB, 1, false>(lo, st);
+    const TokenHalves<T> h(q);
+    const cudaError_t e = wide ? launch_stream<BITS, GS, T, 1, UW, 1, false>(h.lo, st)
+                               : launch_stream<BITS, GS, T, 1, UB, 1, false>(h.lo, st);
     if (e != cudaSuccess) return e;
-    return wide ? launch_stream<BITS, GS, T, 1, UW, 1, false>(hi, st) : launch_stream<BITS, GS, T, 1, UB, 1, false>(hi, st);
+    return wide ? launch_stream<BITS, GS, T, 1, UW, 1, false>(h.hi, st)
+                : launch_stream<BITS, GS, T, 1, UB, 1, false>(h.hi, st);
   } else {
     return cudaErrorNotSupported;
   }
