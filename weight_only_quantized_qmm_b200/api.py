@@ -631,7 +631,7 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     that nothing still running elsewhere uses it, kept until the current
     stream is done with it too."""
     if stream is None or not like.is_cuda:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype == like.dtype else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         t = like.new_empty(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream(like.device))
@@ -661,6 +661,14 @@ def _exactly(t, what: str, shape, dtypes, like: torch.Tensor, stream) -> torch.T
     if t.numel() != n:
         raise ValueError(f"qmm: {what} holds {t.numel()} elements, expected {tuple(shape)}")
     return t
+
+
+def _grads(given, names, shape, dtype, like: torch.Tensor, stream):
+    """The parameter gradients `given`, checked, or new ones (in one piece of
+    memory where each starts on 16 bytes)."""
+    if any(t is not None for t in given) or (shape[0] * shape[1] * dtype.itemsize) % 16:
+        return [_exactly(t, n, shape, (dtype,), like, stream) for t, n in zip(given, names)]
+    return _new((len(names), *shape), dtype, like, stream).unbind(0)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -727,8 +735,7 @@ def qmm_embedding_backward(dy: torch.Tensor, ids: torch.Tensor, qw: QWeight, alp
     dy = _rows_of(dy, "dy", qw.cols, ids.shape, dy.dtype, stream)
     shape = (qw.rows, _groups(qw.cols, qw.group_size))
     g_dtype = g_dtype or (dscales if dscales is not None else qw.scales).dtype
-    dscales = _exactly(dscales, "dscales", shape, (g_dtype,), dy, stream)
-    dbiases = _exactly(dbiases, "dbiases", shape, (g_dtype,), dy, stream)
+    dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, dy, stream)
     ws, nbytes = _workspace("qmm_embedding_backward", workspace, (n, qw.rows, qw.cols), dy, stream)
     dev, (c,) = _structs("qmm_embedding_backward", ("dy", "ids", "dscales", "dbiases", "workspace", "d_status"),
                          (dy, ids, dscales, dbiases, ws, d_status), (("table", qw),))
@@ -781,8 +788,7 @@ def qmm_matmul_backward(dy: torch.Tensor, x: torch.Tensor, qw: QWeight, need_dx:
     dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream) if need_dx else None
     if need_params:
         shape = (N, _groups(K, qw.group_size))
-        dscales = _exactly(dscales, "dscales", shape, (g_dtype,), x2, stream)
-        dbiases = _exactly(dbiases, "dbiases", shape, (g_dtype,), x2, stream)
+        dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, x2, stream)
     else:
         dscales = dbiases = None
     ws, nbytes = _workspace("qmm_matmul_backward", workspace, (M, K, N), x2, stream)
@@ -815,12 +821,9 @@ def qmm_gate_up_silu_backward(dh: torch.Tensor, x: torch.Tensor, g_pre: torch.Te
     gs = gz = us = uz = None
     if need_params:
         shape = (F, _groups(K, gate.group_size))
-        gs, gz = dgate or (None, None)
-        us, uz = dup or (None, None)
-        gs = _exactly(gs, "dgate_scales", shape, (g_dtype,), x2, stream)
-        gz = _exactly(gz, "dgate_biases", shape, (g_dtype,), x2, stream)
-        us = _exactly(us, "dup_scales", shape, (g_dtype,), x2, stream)
-        uz = _exactly(uz, "dup_biases", shape, (g_dtype,), x2, stream)
+        gs, gz, us, uz = _grads((*(dgate or (None, None)), *(dup or (None, None))),
+                                ("dgate_scales", "dgate_biases", "dup_scales", "dup_biases"), shape, g_dtype, x2,
+                                stream)
     ws, nbytes = _workspace("qmm_gate_up_silu_backward", workspace, (M, K, F), x2, stream)
     dev, (cg, cu) = _structs(
         "qmm_gate_up_silu_backward",
