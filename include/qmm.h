@@ -449,10 +449,11 @@ qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int3
                                   qmm_dtype g_dtype, void* workspace, int64_t workspace_bytes, int32_t* d_status,
                                   void* stream);
 
-/* Workspace bytes of qmm_gate_up_silu (-1 for a size outside [0, 2^31 - 1] or
- * M * F or F * K past 2^57): room for both dequantized weights for many
- * tokens, 0 otherwise. */
-int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F);
+/* Workspace bytes of qmm_gate_up_silu (-1 for a size outside [0, 2^31 - 1],
+ * M * F or F * K past 2^57, or a K that cannot be packed in `bits`): room for
+ * both dequantized weights for many tokens and for rows of codes that do not
+ * start on 16 bytes, 0 otherwise. */
+int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits);
 
 /* The gated projection: h[M, F] = SiLU(x . dequant(gate)^T) * (x .
  * dequant(up)^T), SiLU(g) = g / (1 + exp(-g)): the dense form of
@@ -467,9 +468,9 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
                             const qmm_qweight* up, void* h, qmm_dtype h_dtype, void* g_pre, void* u_pre,
                             void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1]
- * or M * N or N * K past 2^57). */
-int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N);
+/* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1],
+ * M * N or N * K past 2^57, or a K that cannot be packed in `bits`). */
+int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits);
 
 /* Gradients of y = x . dequant(W)^T (qmm_matmul, transpose = 1): dx[M, K] = dy .
  * dequant(W) in x_dtype, and dscales, dbiases [N, K / group_size] in g_dtype
@@ -483,8 +484,9 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of qmm_gate_up_silu_backward (-1 for a size outside
- * [0, 2^31 - 1] or M * F or F * K past 2^57). */
-int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F);
+ * [0, 2^31 - 1], M * F or F * K past 2^57, or a K that cannot be packed in
+ * `bits`). */
+int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits);
 
 /* Gradients of the gated projection from its saved g_pre and u_pre: with
  * p = 1 / (1 + exp(-g)), du = dh * g * p and dg = dh * u * p * (1 + g * (1 - p)),

@@ -75,8 +75,8 @@ def test_gate_up(L):
 def test_backward(L):
     for need in (L.qmm_matmul_backward_workspace_bytes, L.qmm_gate_up_silu_backward_workspace_bytes,
                  L.qmm_gate_up_silu_workspace_bytes):
-        assert need(0, 32, 0) >= 0 and need(100, 128, 77) >= 0
-        assert need(-1, 128, 8) == need(8, 2 ** 31, 8) == need(8, 128, -1) == -1
+        assert need(0, 32, 0, 4) >= 0 and need(100, 128, 77, 3) >= 0
+        assert need(-1, 128, 8, 4) == need(8, 2 ** 31, 8, 4) == need(8, 128, -1, 4) == need(8, 33, 8, 3) == -1
 
     def one(w=None, dy=A, x=A, xt=BF, M=2, K=128, dx=A, ds=A, dz=A, g=BF, ws=A, nb=1 << 40):
         w = w or qw()

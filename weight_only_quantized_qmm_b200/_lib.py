@@ -122,15 +122,15 @@ def load() -> ctypes.CDLL:
     L.qmm_embedding_backward_workspace_bytes.restype = i64
     L.qmm_embedding_backward.argtypes = [vp, c_int, vp, i64, qwp, ctypes.c_float, vp, vp, c_int, vp, i64, vp, vp]
     L.qmm_embedding_backward.restype = c_int
-    L.qmm_gate_up_silu_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qmm_gate_up_silu_workspace_bytes.argtypes = [i64, i64, i64, c_int]
     L.qmm_gate_up_silu_workspace_bytes.restype = i64
     L.qmm_gate_up_silu.argtypes = [vp, c_int, i64, i64, qwp, qwp, vp, c_int, vp, vp, vp, i64, vp]
     L.qmm_gate_up_silu.restype = c_int
-    L.qmm_matmul_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qmm_matmul_backward_workspace_bytes.argtypes = [i64, i64, i64, c_int]
     L.qmm_matmul_backward_workspace_bytes.restype = i64
     L.qmm_matmul_backward.argtypes = [vp, vp, c_int, i64, i64, qwp, vp, vp, vp, c_int, vp, i64, vp]
     L.qmm_matmul_backward.restype = c_int
-    L.qmm_gate_up_silu_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.qmm_gate_up_silu_backward_workspace_bytes.argtypes = [i64, i64, i64, c_int]
     L.qmm_gate_up_silu_backward_workspace_bytes.restype = i64
     L.qmm_gate_up_silu_backward.argtypes = [vp, vp, vp, vp, c_int, i64, i64, qwp, qwp, vp, vp, vp, vp, vp, c_int, vp,
                                             i64, vp]

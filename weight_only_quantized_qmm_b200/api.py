@@ -762,7 +762,7 @@ def qmm_gate_up_silu(x: torch.Tensor, gate: QWeight, up: QWeight, y_dtype: torch
     if save or g_pre is not None or u_pre is not None:
         g_pre = _exactly(g_pre, "g_pre", shape, (x.dtype,), x2, stream)
         u_pre = _exactly(u_pre, "u_pre", shape, (x.dtype,), x2, stream)
-    ws, nbytes = _workspace("qmm_gate_up_silu", workspace, (M, K, F), x2, stream)
+    ws, nbytes = _workspace("qmm_gate_up_silu", workspace, (M, K, F, gate.bits), x2, stream)
     dev, (cg, cu) = _structs("qmm_gate_up_silu", ("x", "out", "g_pre", "u_pre", "workspace"),
                              (x2, out, g_pre, u_pre, ws), (("gate", gate), ("up", up)))
     rc = _lib.load().qmm_gate_up_silu(
@@ -791,7 +791,7 @@ def qmm_matmul_backward(dy: torch.Tensor, x: torch.Tensor, qw: QWeight, need_dx:
         dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, x2, stream)
     else:
         dscales = dbiases = None
-    ws, nbytes = _workspace("qmm_matmul_backward", workspace, (M, K, N), x2, stream)
+    ws, nbytes = _workspace("qmm_matmul_backward", workspace, (M, K, N, qw.bits), x2, stream)
     dev, (c,) = _structs("qmm_matmul_backward", ("dy", "x", "dx", "dscales", "dbiases", "workspace"),
                          (dy2, x2, dx, dscales, dbiases, ws), (("w", qw),))
     rc = _lib.load().qmm_matmul_backward(
@@ -824,7 +824,7 @@ def qmm_gate_up_silu_backward(dh: torch.Tensor, x: torch.Tensor, g_pre: torch.Te
         gs, gz, us, uz = _grads((*(dgate or (None, None)), *(dup or (None, None))),
                                 ("dgate_scales", "dgate_biases", "dup_scales", "dup_biases"), shape, g_dtype, x2,
                                 stream)
-    ws, nbytes = _workspace("qmm_gate_up_silu_backward", workspace, (M, K, F), x2, stream)
+    ws, nbytes = _workspace("qmm_gate_up_silu_backward", workspace, (M, K, F, gate.bits), x2, stream)
     dev, (cg, cu) = _structs(
         "qmm_gate_up_silu_backward",
         ("dh", "x", "g_pre", "u_pre", "dx", "dgate_scales", "dgate_biases", "dup_scales", "dup_biases", "workspace"),

@@ -18,13 +18,13 @@
 
 namespace qmm {
 namespace pg {
-cudaError_t dispatch_b2(int, bool, const Args&, const CUtensorMap (&)[4], int, cudaStream_t);
-cudaError_t dispatch_b3(int, bool, const Args&, const CUtensorMap (&)[4], int, cudaStream_t);
-cudaError_t dispatch_b4(int, bool, const Args&, const CUtensorMap (&)[4], int, cudaStream_t);
-cudaError_t dispatch_b6(int, bool, const Args&, const CUtensorMap (&)[4], int, cudaStream_t);
-cudaError_t dispatch_b8(int, bool, const Args&, const CUtensorMap (&)[4], int, cudaStream_t);
-cudaError_t dispatch_dense(int, const Args&, const CUtensorMap (&)[4], int, cudaStream_t);
-cudaError_t dequant_parts(int op, int bits, const Args& p, void* ws, CUtensorMap* tm, cudaStream_t st);
+cudaError_t dispatch_b2(int, bool, Args&, Maps&, int, cudaStream_t);
+cudaError_t dispatch_b3(int, bool, Args&, Maps&, int, cudaStream_t);
+cudaError_t dispatch_b4(int, bool, Args&, Maps&, int, cudaStream_t);
+cudaError_t dispatch_b6(int, bool, Args&, Maps&, int, cudaStream_t);
+cudaError_t dispatch_b8(int, bool, Args&, Maps&, int, cudaStream_t);
+cudaError_t dispatch_dense(int, const Args&, const Maps&, int, cudaStream_t);
+cudaError_t dequant_parts(int op, int bits, const Args& p, void* ws, Maps& tm, cudaStream_t st);
 }  // namespace pg
 
 namespace ffn {
@@ -112,7 +112,7 @@ static pg::Args args_of(int64_t M, int64_t K, const qmm_qweight* w0, const qmm_q
 }
 
 // bits == 0: weights dequantized beforehand
-static cudaError_t run(int op, int bits, bool pair, pg::Args& p, const CUtensorMap (&tm)[4], cudaStream_t st) {
+static cudaError_t run(int op, int bits, bool pair, pg::Args& p, pg::Maps& tm, cudaStream_t st) {
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * (op == pg::DP ? p.parts : 1);
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
   int clusters = (int)std::min<int64_t>(tiles, qmm_host::num_sms() / 2);
@@ -137,7 +137,8 @@ static int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // Whether the weights are dequantized into the workspace first: the pass costs
 // about 60 us for gate and up of 4096 x 14336, and the product then runs at
 // 1375 TFLOP/s instead of 1070 (measured at 4096 and 1024 tokens).
-static bool dense_first(int64_t M) { return M >= 1536; }
+// The kernels that dequantize themselves want rows of codes on 16 bytes.
+static bool dense_first(int64_t M, int64_t K, int bits) { return M >= 1536 || (K * bits) % 128 != 0; }
 
 // dense: room for both dequantized weights, or null
 static cudaError_t forward(const void* x, int x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
@@ -152,11 +153,11 @@ static cudaError_t forward(const void* x, int x_dtype, int64_t M, int64_t K, con
   p.out[1] = gp;
   p.out[2] = upre;
   p.out_dtype = h_dtype;
-  CUtensorMap tm[4];
-  if (!pg::make_map(&tm[0], x, p.f16, M, K, K, 128)) return cudaErrorInvalidValue;
-  tm[1] = tm[2] = tm[3] = tm[0];
+  pg::Maps tm;
+  if (!pg::make_map(&tm.a[0], x, p.f16, M, K, K, 128)) return cudaErrorInvalidValue;
+  tm.a[1] = tm.b[0] = tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.a[0];
   if (dense) {
-    const cudaError_t e = pg::dequant_parts(pg::FWD, gate->bits, p, dense, &tm[2], st);
+    const cudaError_t e = pg::dequant_parts(pg::FWD, gate->bits, p, dense, tm, st);
     return e != cudaSuccess ? e : run(pg::FWD, 0, true, p, tm, st);
   }
   return run(pg::FWD, gate->bits, pair, p, tm, st);
@@ -174,7 +175,7 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
     for (int i = 0; i < (w1 ? 4 : 2) && grads[0] && bytes && e == cudaSuccess; ++i) e = cudaMemsetAsync(grads[i], 0, bytes, st);
     return e;
   }
-  CUtensorMap tm[4];
+  pg::Maps tm;
   if (dx) {
     pg::Args p = args_of(M, K, w0, w1, x_dtype);
     const bool pair = dense || M > 128;
@@ -183,10 +184,10 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
     p.steps = p.parts * ceil_div(N, pg::kBK);
     p.out[0] = dx;
     p.out_dtype = x_dtype;
-    if (!pg::make_map(&tm[0], dy0, p.f16, M, N, ld, 128) || !pg::make_map(&tm[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 128))
+    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 128) || !pg::make_map(&tm.a[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 128))
       return cudaErrorInvalidValue;
-    tm[2] = tm[3] = tm[0];
-    cudaError_t e = dense ? pg::dequant_parts(pg::DX, w0->bits, p, dense, &tm[2], st) : cudaSuccess;
+    tm.b[0] = tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.a[0];
+    cudaError_t e = dense ? pg::dequant_parts(pg::DX, w0->bits, p, dense, tm, st) : cudaSuccess;
     if (e == cudaSuccess) e = run(pg::DX, dense ? 0 : w0->bits, pair, p, tm, st);
     if (e != cudaSuccess) return e;
   }
@@ -197,10 +198,10 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
     p.steps = ceil_div(M, pg::kBK);
     for (int i = 0; i < 4; ++i) p.out[i] = grads[i];
     p.out_dtype = g_dtype;
-    if (!pg::make_map(&tm[0], dy0, p.f16, M, N, ld, 64) || !pg::make_map(&tm[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 64) ||
-        !pg::make_map(&tm[2], x, p.f16, M, K, K, 64))
+    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 64) || !pg::make_map(&tm.a[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 64) ||
+        !pg::make_map(&tm.b[0], x, p.f16, M, K, K, 64))
       return cudaErrorInvalidValue;
-    tm[3] = tm[2];
+    tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.b[0];
     return run(pg::DP, w0->bits, true, p, tm, st);
   }
   return cudaSuccess;
@@ -209,7 +210,9 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
 static int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
 static int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 // bytes of `parts` dequantized weights for M tokens
-static int64_t dense_bytes(int64_t M, int64_t K, int64_t N, int parts) { return dense_first(M) ? parts * N * K * 2 : 0; }
+static int64_t dense_bytes(int64_t M, int64_t K, int64_t N, int bits, int parts) {
+  return dense_first(M, K, bits) ? parts * N * K * 2 : 0;
+}
 
 }  // namespace ffn
 }  // namespace qmm
@@ -217,6 +220,8 @@ static int64_t dense_bytes(int64_t M, int64_t K, int64_t N, int parts) { return 
 using namespace qmm_host;
 
 namespace {
+
+constexpr int64_t kFewTokens = 16;  // tokens of the streaming kernels
 
 bool i32(int64_t v) { return v >= 0 && v <= (int64_t)INT32_MAX; }
 // M rows of n elements (padded) and n rows of K, all within 2^57 elements
@@ -250,9 +255,9 @@ qmm_status check_pair(const qmm_qweight* gate, const qmm_qweight* up, qmm_dtype 
 
 extern "C" {
 
-int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F) {
-  if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F)) return -1;
-  return qmm::ffn::dense_bytes(M, K, F, 2);
+int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits) {
+  if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F) || qmm_packed_words_per_row(K, bits) < 0) return -1;
+  return M > kFewTokens ? qmm::ffn::dense_bytes(M, K, F, bits, 2) : 0;
 }
 
 qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
@@ -262,7 +267,7 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
   if (s != QMM_OK) return s;
   if (!dtype_ok(h_dtype) || (h_dtype != x_dtype && h_dtype != QMM_F32)) return QMM_ERR_DTYPE;
   if ((g_pre == nullptr) != (u_pre == nullptr)) return QMM_ERR_INVALID_ARG;
-  const int64_t need = qmm_gate_up_silu_workspace_bytes(M, K, gate->rows);
+  const int64_t need = qmm_gate_up_silu_workspace_bytes(M, K, gate->rows, gate->bits);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M == 0 || gate->rows == 0) return QMM_OK;
   if (need > 0 && !aligned16(workspace)) return QMM_ERR_ALIGNMENT;
@@ -270,19 +275,19 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
   s = qmm_device_check();
   if (s != QMM_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
-  if (M <= 16) {  // few tokens: the streaming kernels, both matrices in one pass
+  if (M <= kFewTokens) {  // the streaming kernels, both matrices in one pass
     const qmm::QgemvParams p = qmm::make_gated_params(x, x_dtype, M, K, gate, up, h, h_dtype, g_pre, u_pre);
     const cudaError_t e = qmm::launch_qgemv(p, gate->bits, gate->group_size, x_dtype, true, st);
-    if (e != cudaErrorInvalidValue) return launch_status(e);
+    return e == cudaErrorInvalidValue ? QMM_ERR_UNSUPPORTED : launch_status(e);
   }
   return launch_status(qmm::ffn::forward(x, x_dtype, M, K, gate, up, h, h_dtype, g_pre, u_pre,
-                                         qmm::ffn::dense_first(M) ? workspace : nullptr, st));
+                                         need > 0 ? workspace : nullptr, st));
 }
 
-int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (!i32(M) || !i32(K) || !i32(N) || !fits(M, K, N)) return -1;
+int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits) {
+  if (!i32(M) || !i32(K) || !i32(N) || !fits(M, K, N) || qmm_packed_words_per_row(K, bits) < 0) return -1;
   // rows of dy that do not start on 16 bytes are copied to ones that do
-  return qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) + qmm::ffn::dense_bytes(M, K, N, 1);
+  return qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) + qmm::ffn::dense_bytes(M, K, N, bits, 1);
 }
 
 qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype, int64_t M, int64_t K,
@@ -292,7 +297,7 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
   if (s != QMM_OK) return s;
   if (!dtype_ok(g_dtype) || (g_dtype != x_dtype && g_dtype != QMM_F32)) return QMM_ERR_DTYPE;
   if ((dscales == nullptr) != (dbiases == nullptr) || (!dx && !dscales)) return QMM_ERR_INVALID_ARG;
-  const int64_t need = qmm_matmul_backward_workspace_bytes(M, K, w->rows);
+  const int64_t need = qmm_matmul_backward_workspace_bytes(M, K, w->rows, w->bits);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M > 0 && w->rows > 0 && (!aligned16(dy) || !aligned16(x))) return QMM_ERR_ALIGNMENT;
   if ((dx && !aligned16(dx)) || (dscales && (!aligned16(dscales) || !aligned16(dbiases))) ||
@@ -310,13 +315,13 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
     if (e != cudaSuccess) return launch_status(e);
     dy = workspace;
   }
-  void* dense = qmm::ffn::dense_first(M) ? static_cast<char*>(workspace) + qmm::ffn::align16(N % 8 ? M * ld * 2 : 0) : nullptr;
+  void* dense = qmm::ffn::dense_first(M, K, w->bits) ? static_cast<char*>(workspace) + qmm::ffn::align16(N % 8 ? M * ld * 2 : 0) : nullptr;
   return launch_status(qmm::ffn::backward(dy, nullptr, ld, x, x_dtype, M, K, w, nullptr, dx, grads, g_dtype, dense, st));
 }
 
-int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F) {
-  if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F)) return -1;
-  return qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) + qmm::ffn::dense_bytes(M, K, F, 2);  // dg and du first
+int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits) {
+  if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F) || qmm_packed_words_per_row(K, bits) < 0) return -1;
+  return qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) + qmm::ffn::dense_bytes(M, K, F, bits, 2);  // dg and du first
 }
 
 qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* g_pre, const void* u_pre,
@@ -332,7 +337,7 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
     if ((grads[i] == nullptr) != (grads[0] == nullptr)) return QMM_ERR_INVALID_ARG;
   if (!dx && !grads[0]) return QMM_ERR_INVALID_ARG;
   const int64_t F = gate->rows;
-  const int64_t need = qmm_gate_up_silu_backward_workspace_bytes(M, K, F);
+  const int64_t need = qmm_gate_up_silu_backward_workspace_bytes(M, K, F, gate->bits);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M > 0 && F > 0 && (!aligned16(dh) || !aligned16(x) || !aligned16(g_pre) || !aligned16(u_pre)))
     return QMM_ERR_ALIGNMENT;
@@ -352,7 +357,7 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
             : qmm::ffn::act_grad<__half>(dh, g_pre, u_pre, n, (int)F, (int)ld, dg, du, st);
     if (e != cudaSuccess) return launch_status(e);
   }
-  void* dense = qmm::ffn::dense_first(M) ? static_cast<char*>(workspace) + qmm::ffn::align16(2 * M * ld * 2) : nullptr;
+  void* dense = qmm::ffn::dense_first(M, K, gate->bits) ? static_cast<char*>(workspace) + qmm::ffn::align16(2 * M * ld * 2) : nullptr;
   return launch_status(qmm::ffn::backward(dg, du, ld, x, x_dtype, M, K, gate, up, dx, grads, g_dtype, dense, st));
 }
 

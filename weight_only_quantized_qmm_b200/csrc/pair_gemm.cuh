@@ -22,14 +22,17 @@
 //
 // FWD and DX take weights dequantized beforehand (B = 0: many tokens, where the
 // extra pass is small beside the product and the two TMA-fed operands run at
-// the tensor cores' rate), or dequantize in the kernel: sixteen warps keep four units (32
-// codes of one row) in flight in registers, form (OFF + q) - OFF and one fused
-// q * s + z in the activations' type (one rounding), and write the swizzled
-// operand tile: K-major for FWD, MN-major for DX (the same packed rows, read
-// along their length both times).
+// the tensor cores' rate), or dequantize in the kernel: the packed codes of each
+// step arrive in a ring of their own (TMA boxes, swizzled at their width), the
+// scales and biases too where their rows start on 16 bytes; sixteen warps turn 64
+// codes of one row per thread into (OFF + q) - OFF and one fused q * s + z in the
+// activations' type (one rounding), and write the swizzled operand tile:
+// K-major for FWD, MN-major for DX (the same packed rows, read along their length
+// both times).
 //
-// Warps: 0 TMA producer; 1 TMEM owner and MMA issuer (PAIR: of the leader
-// CTA); 2.. epilogue (4 warps, DP 8); then the 16 dequant warps.
+// Warps: 0 TMA producer of the activations; 1 TMEM owner and MMA issuer (PAIR:
+// of the leader CTA); 2.. epilogue (4 warps, DP 8); then the producer of the
+// codes and the 16 dequant warps.
 // Every wait is bounded; after one that gave up the tiles are written as NaN.
 #pragma once
 
@@ -62,17 +65,40 @@ struct Cfg {
   static constexpr bool DENSE = OP == DP || B == 0;                // both operands come by TMA
   static constexpr int EPI = OP == DP ? 8 : 4;                     // epilogue warps
   static constexpr int DEQ = DENSE ? 0 : kDeqWarps;
-  static constexpr int THREADS = (2 + EPI + DEQ) * 32;
+  static constexpr int THREADS = (2 + EPI + (DENSE ? 0 : 1) + DEQ) * 32;
   static constexpr int A_BYTES = kTile;                            // 128 rows of A per CTA
   static constexpr int B_BYTES = PAIR ? kTile : 2 * kTile;         // 128 or 256 of B
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = PAIR ? 6 : 4;
-  static constexpr int BAR0 = STAGES * STAGE;
-  static constexpr int SMEM = 1024 + BAR0 + 256;                   // + alignment slack, barriers
+  static constexpr int STAGES = DENSE ? 6 : PAIR ? 5 : 3;
+  // the ring of packed codes, one slot a step.  A box: FWD, 128 rows of 64
+  // codes (3-bit: of 128, whose 48 bytes TMA can copy; each step reads its
+  // half); DX, 64 rows of 128 codes.  Single CTAs have two boxes.
+  static constexpr int ROW = OP == FWD ? (B == 3 ? 48 : 8 * B) : 16 * B;
+  static constexpr int BOX_ROWS = OP == FWD ? 128 : 64;
+  static constexpr int BOX = BOX_ROWS * ROW;
+  static constexpr int BOXES = PAIR ? 1 : 2;
+  // swizzle: 16-byte piece c of row r sits at c ^ swz(r)
+  static constexpr int SWZ = ROW == 32 || ROW == 64 || ROW == 128 ? ROW : 0;
+  // scales and biases, 8 groups (16 bytes) of each row: DX, those of the step's 64
+  // rows, in the slot of its codes; FWD, windows of 8 groups in a ring of two
+  static constexpr int SB = BOX_ROWS * 16;                         // one array, one box
+  static constexpr int SLOT = DENSE ? 1024 : (BOXES * BOX + (OP == DX ? 2 * SB : 0) + 1023) / 1024 * 1024;
+  static constexpr int WINDOW = OP == FWD ? 2 * BOXES * SB : 0;
+  static constexpr int CODE0 = STAGES * STAGE;
+  static constexpr int AVAIL = 227 * 1024 - 2048 - CODE0 - 2 * WINDOW;
+  static constexpr int SLOTS = DENSE ? 0 : AVAIL / SLOT < 8 ? AVAIL / SLOT : 8;
+  static constexpr int WIN0 = CODE0 + SLOTS * SLOT;
+  static constexpr int BAR0 = WIN0 + (DENSE ? 0 : 2 * WINDOW);
+  static constexpr int BARS = 2 * STAGES + 5 + 2 * SLOTS + 2;
+  static constexpr int SMEM = 1024 + BAR0 + 512;                   // + alignment slack, barriers
   static_assert(!DENSE || PAIR, "these run on CTA pairs");
-  static_assert(8 * (2 * STAGES + 5) + 8 <= 256, "barriers, TMEM slot and abort flag");
+  static_assert(DENSE || SLOTS >= 3, "room for the codes");
+  static_assert(8 * BARS + 8 <= 512, "barriers, TMEM slot and abort flag");
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(PAIR || 128 * 256 * 4 <= BAR0, "a partial tile fits the stages");
+  static_assert(PAIR || 128 * 256 * 4 <= CODE0, "a partial tile fits the stages");
+  __device__ static constexpr int swz(int r) {
+    return SWZ == 32 ? (r >> 2) & 1 : SWZ == 64 ? (r >> 1) & 3 : SWZ == 128 ? r & 7 : 0;
+  }
 };
 
 struct Weight {
@@ -92,6 +118,13 @@ struct Args {
   void* out[4];           // FWD: h, g, u; DX: dx; DP: dscales, dbiases of both parts
   int out_dtype;          // FWD: of h; DP
   int f16;                // operands are f16 (otherwise bf16)
+  int sb_tma;             // scales and biases come by TMA (rows of a multiple of 8 groups)
+};
+
+struct Maps {
+  CUtensorMap a[2];  // FWD: x; DX, DP: dy of each part
+  CUtensorMap b[2];  // packed codes or dequantized weights of each part; DP: x
+  CUtensorMap s[2], z[2];
 };
 
 // ------------------------------------------------------------------ PTX
@@ -206,13 +239,6 @@ __device__ __forceinline__ float4 lds_cluster(uint32_t a) {
 }
 
 // ------------------------------------------------------------------ dequantize
-// 32 codes of one row (B words) and their group's scale and bias
-template <int B>
-struct Unit {
-  uint32_t w[B];
-  uint16_t s, z;
-};
-
 template <typename T>
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -281,23 +307,59 @@ __device__ __forceinline__ uint4 dequant8(const uint32_t (&w)[B], uint16_t scale
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// 32 codes, read once: past L1
+// 32 codes of a row in global memory
 template <int B>
 __device__ __forceinline__ void load_words(const uint32_t* src, uint32_t (&w)[B]) {
   if constexpr (B % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < B; i += 4)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "l"(src + i));
+    for (int i = 0; i < B; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i));
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
   } else if constexpr (B % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < B; i += 2)
-      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "l"(src + i));
+    for (int i = 0; i < B; i += 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + i));
+      w[i] = v.x; w[i + 1] = v.y;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < B; ++i)
-      asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[i]) : "l"(src + i));
+    for (int i = 0; i < B; ++i) w[i] = __ldg(src + i);
+  }
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint16_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+// 64 codes (8 B bytes) from byte `off` of the row at `row`, whose 16-byte pieces
+// are swizzled by `swz`
+template <int B>
+__device__ __forceinline__ void read_codes(uint32_t row, int off, int swz, uint32_t (&w)[2][B]) {
+  uint32_t* d = &w[0][0];
+  if constexpr (B == 3) {  // 24 bytes, 8-byte aligned, never swizzled
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint2 v = lds_v2(row + off + 8 * i);
+      d[2 * i] = v.x;
+      d[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < B / 2; ++i) {
+      const uint4 v = lds_v4(row + ((((off >> 4) + i) ^ swz) << 4));
+      d[4 * i] = v.x; d[4 * i + 1] = v.y; d[4 * i + 2] = v.z; d[4 * i + 3] = v.w;
+    }
   }
 }
 
@@ -357,9 +419,7 @@ __device__ __forceinline__ void store_h8(const Args& p, int m, int n, const floa
 
 template <int OP, int B, typename T, bool PAIR>
 __global__ void __launch_bounds__(Cfg<OP, B, PAIR>::THREADS, 1)
-pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap tma0,
-                 const __grid_constant__ CUtensorMap tma1, const __grid_constant__ CUtensorMap tmb0,
-                 const __grid_constant__ CUtensorMap tmb1) {
+pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm) {
   using C = Cfg<OP, B, PAIR>;
   constexpr int S = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -370,7 +430,10 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
   const uint32_t accf0 = empty0 + 8 * S;     // [2] accumulator complete
   const uint32_t tfree0 = accf0 + 16;        // [2] accumulator read out
   const uint32_t drain = tfree0 + 16;        // every issued MMA complete
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR0 + 8 * (2 * S + 5));
+  const uint32_t cfull0 = drain + 8;         // [SLOTS] the step's codes are in
+  const uint32_t cempty0 = cfull0 + 8 * C::SLOTS;   // [SLOTS] and dequantized
+  const uint32_t wfull0 = cempty0 + 8 * C::SLOTS;   // [2] a window of scales and biases is in (FWD)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR0 + 8 * C::BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -388,9 +451,9 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      // the producer, and the dequant warps that fill the stage (all 16 of a
-      // single CTA; 8 of each CTA of a pair, which take turns by stage)
-      mbar_init(full0 + 8 * s, 1 + (C::DENSE ? 0 : kDeqWarps));
+      // the producer, and the dequant warps that fill the stage (4 of each CTA
+      // of a pair, 8 of a single one)
+      mbar_init(full0 + 8 * s, 1 + (C::DENSE ? 0 : 8));
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -398,6 +461,12 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
       mbar_init(tfree0 + 8 * b, C::EPI * (PAIR ? 2 : 1));
     }
     mbar_init(drain, 1);
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(cfull0 + 8 * s, 1);
+      mbar_init(cempty0 + 8 * s, PAIR ? 4 : 8);
+    }
+    mbar_init(wfull0, 1);
+    mbar_init(wfull0 + 8, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -439,25 +508,25 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
           const uint32_t a = stage0 + s * C::STAGE, bar = lfull0 + 8 * s;
           if (leader) mbar_arrive_expect_tx(full0 + 8 * s, kTx);
           if constexpr (OP == DP) {
-            const CUtensorMap* ma = tl.part ? &tma1 : &tma0;
+            const CUtensorMap* ma = &tm.a[tl.part];
             const int col = tl.n0 + 128 * (int)rank;
             tma_2d<PAIR>(a, ma, row, i * kBK, bar);
             tma_2d<PAIR>(a + 8192, ma, row + 64, i * kBK, bar);
-            tma_2d<PAIR>(a + C::A_BYTES, &tmb0, col, i * kBK, bar);
-            tma_2d<PAIR>(a + C::A_BYTES + 8192, &tmb0, col + 64, i * kBK, bar);
+            tma_2d<PAIR>(a + C::A_BYTES, &tm.b[0], col, i * kBK, bar);
+            tma_2d<PAIR>(a + C::A_BYTES + 8192, &tm.b[0], col + 64, i * kBK, bar);
           } else if constexpr (OP == DX) {
             const bool second = i >= half;
             const int n = (second ? i - half : i) * kBK;
-            tma_2d<PAIR>(a, second ? &tma1 : &tma0, n, row, bar);
+            tma_2d<PAIR>(a, &tm.a[second], n, row, bar);
             if constexpr (C::DENSE) {
-              const CUtensorMap* mb = second ? &tmb1 : &tmb0;
+              const CUtensorMap* mb = &tm.b[second];
               const int col = tl.n0 + 128 * (int)rank;
               tma_2d<PAIR>(a + C::A_BYTES, mb, col, n, bar);
               tma_2d<PAIR>(a + C::A_BYTES + 8192, mb, col + 64, n, bar);
             }
           } else {
-            tma_2d<PAIR>(a, &tma0, i * kBK, row, bar);
-            if constexpr (C::DENSE) tma_2d<PAIR>(a + C::A_BYTES, rank ? &tmb1 : &tmb0, i * kBK, tl.n0, bar);
+            tma_2d<PAIR>(a, &tm.a[0], i * kBK, row, bar);
+            if constexpr (C::DENSE) tma_2d<PAIR>(a + C::A_BYTES, &tm.b[rank], i * kBK, tl.n0, bar);
           }
           ++issued;
           if (++s == S) s = 0, ++u;
@@ -642,93 +711,179 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtenso
       }
     }
   } else if constexpr (!C::DENSE) {
-    // ---------------- dequantize ----------------
-    constexpr int kAhead = B == 8 ? 2 : 4;  // units in flight per thread
-    constexpr int STEP = PAIR ? 2 : 1;      // a pair's two sets of 8 warps take turns by stage
-    const int dw = warp - 2 - C::EPI;
-    const uint32_t lfull0 = PAIR ? map_rank(full0, 0) : full0;
-    const int wpr = (p.K >> 5) * B;
-    const int64_t G = p.K >> p.lgs;
-    const int half = p.steps / p.parts;
-    // this thread's unit in a stage and its 16-byte chunks in the operand tile.
-    // Lanes are laid so that eight consecutive ones write eight different bank
-    // groups, and the lanes that share a row read one 32-byte piece of it.
-    int ur, uc;          // FWD: row of the 128 (256) and which half of its 64 codes
-    uint32_t at;         // byte offset of chunk 0 before the swizzle
-    int swz;
-    if constexpr (OP == FWD) {
-      ur = (PAIR ? dw & 7 : dw) * 16 + (lane >> 1);
-      uc = lane & 1;
-      at = (uint32_t)(ur * 128);
-      swz = ur & 7;
-    } else {             // DX: row of the 64 and which 32 of the tile's columns
-      ur = (dw & 7) * 8 + ((lane >> 1) & 3) + ((lane >> 4) << 2);
-      uc = (lane & 1) | ((lane >> 3) & 1) << 1 | (PAIR ? 0 : (dw >> 3) << 2);
-      at = (uint32_t)((uc >> 1) * 8192 + ur * 128);
-      swz = ur & 7;
-    }
-    const int ch0 = (uc & 1) * 4;  // first chunk of the unit in its 128 bytes
-
-    // the cursor of the loads: step i of tile lt
-    int li = PAIR ? (dw >> 3) : 0, llt = 0;
-    Tile ltl{};
-    auto settle = [&]() {
-      while (li >= nk && llt < my_tiles) li -= nk, ++llt;
-      if (llt < my_tiles) ltl = tile_of<OP, PAIR>(p, cluster + llt * clusters);
-    };
-    auto load = [&](Unit<B>& un) {
-      bool ok = llt < my_tiles;
-      const int i = s_lo + li;
-      int64_t row;
-      int k, part;
-      if constexpr (OP == FWD) {
-        row = ltl.n0 + (ur & 127);
-        part = PAIR ? (int)rank : ur >> 7;
-        k = i * kBK + uc * 32;
-      } else {
-        part = i >= half ? 1 : 0;
-        row = (int64_t)(part ? i - half : i) * kBK + ur;
-        k = ltl.n0 + (PAIR ? 128 * (int)rank : 0) + uc * 32;
-      }
-      ok = ok && row < p.N && k < p.K;
-      if (ok) {
-        const Weight& w = p.w[part];
-        load_words<B>(w.packed + row * wpr + (k >> 5) * B, un.w);
-        un.s = __ldg(reinterpret_cast<const uint16_t*>(w.scales) + row * G + (k >> p.lgs));
-        un.z = __ldg(reinterpret_cast<const uint16_t*>(w.biases) + row * G + (k >> p.lgs));
-      } else {  // past the weight: zeros, which the sum's padding is multiplied by
+    const int half = p.steps / p.parts;    // DX: steps of one part
+    const int spw = p.lgs - 3;             // log2 of the steps of a window: 8 groups
+    if (warp == 2 + C::EPI) {
+      // ---------------- producer of the codes, scales and biases ----------------
+      if (lane == 0) {
+        const uint32_t sb_tx = p.sb_tma ? 2 * C::SB : 0;
+        int j = 0, done = 0, win = 0, win_start = 0;  // done: steps known to be dequantized
+        bool stop = false;
+        auto reach = [&](int upto) {
+          for (; done < upto; ++done)
+            if (!mbar_wait_abortable(cempty0 + 8 * (done % C::SLOTS), (done / C::SLOTS) & 1, kSpins, abort_flag))
+              return false;
+          return true;
+        };
+        for (int lt = 0; lt < my_tiles && !stop; ++lt) {
+          const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
+          for (int i = s_lo; i < s_hi; ++i, ++j) {
+            if (OP == FWD && p.sb_tma && (i == s_lo || (i & ((1 << spw) - 1)) == 0)) {
+              // the window before the last one makes room
+              if (!reach(win_start)) {
+                stop = true;
+                break;
+              }
+              const uint32_t d = stage0 + C::WIN0 + (win & 1) * C::WINDOW, bar = wfull0 + 8 * (win & 1);
+              const int g = ((i * kBK) >> p.lgs) & ~7;
+              mbar_arrive_expect_tx(bar, C::WINDOW);
 #pragma unroll
-        for (int j = 0; j < B; ++j) un.w[j] = 0u;
-        un.s = un.z = 0;
-      }
-      li += STEP;
-      if (li >= nk) settle();
-    };
-    settle();
-    Unit<B> ring[kAhead];
+              for (int x = 0; x < C::BOXES; ++x) {
+                const int part = PAIR ? (int)rank : x;
+                tma_2d<false>(d + (2 * x) * C::SB, &tm.s[part], g, tl.n0, bar);
+                tma_2d<false>(d + (2 * x + 1) * C::SB, &tm.z[part], g, tl.n0, bar);
+              }
+              ++win;
+              win_start = j;
+            }
+            if (!reach(j - C::SLOTS + 1)) {
+              stop = true;
+              break;
+            }
+            const uint32_t d = stage0 + C::CODE0 + (j % C::SLOTS) * C::SLOT, bar = cfull0 + 8 * (j % C::SLOTS);
+            mbar_arrive_expect_tx(bar, C::BOXES * C::BOX + (OP == DX ? sb_tx : 0u));
+            if constexpr (OP == FWD) {
+              const int w = B == 3 ? (i >> 1) * 12 : i * 2 * B;  // first word
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) load(ring[a]);
-    const int total = my_tiles * nk;
-    for (int j0 = PAIR ? (dw >> 3) : 0; j0 < total; j0 += STEP * kAhead) {
+              for (int x = 0; x < C::BOXES; ++x)
+                tma_2d<false>(d + x * C::BOX, &tm.b[PAIR ? (int)rank : x], w, tl.n0, bar);
+            } else {
+              const int part = i >= half, n = (part ? i - half : i) * kBK;
+              const int col = tl.n0 + (PAIR ? 128 * (int)rank : 0);
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int j = j0 + a * STEP;
-        if (j < total) {
-          const int s = j % S, u = j / S;
-          if (u > 0 && !mbar_wait_abortable(empty0 + 8 * s, (u - 1) & 1, kSpins, abort_flag)) *abort_flag = 1;
-          const uint32_t dst = stage0 + (uint32_t)(s * C::STAGE + C::A_BYTES) + at;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sts_v4(dst + (uint32_t)(((ch0 + c) ^ swz) << 4), dequant8<B, T>(ring[a].w, ring[a].s, ring[a].z, c));
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR)
-              arrive_remote(lfull0 + 8 * s);
-            else
-              mbar_arrive(full0 + 8 * s);
+              for (int x = 0; x < C::BOXES; ++x)
+                tma_2d<false>(d + x * C::BOX, &tm.b[part], ((col + 128 * x) >> 5) * B, n, bar);
+              if (p.sb_tma) {
+                const int g = (col >> p.lgs) & ~7;
+                tma_2d<false>(d + C::BOXES * C::BOX, &tm.s[part], g, n, bar);
+                tma_2d<false>(d + C::BOXES * C::BOX + C::SB, &tm.z[part], g, n, bar);
+              }
+            }
           }
-          load(ring[a]);
         }
+        if (stop) {
+          // (as the other producer: copies may be landing)
+          *abort_flag = 1;
+          for (int q = max(0, j - C::SLOTS); q < j; ++q)
+            mbar_wait_n(cfull0 + 8 * (q % C::SLOTS), (q / C::SLOTS) & 1, 1u << 12);
+          for (int q = max(0, win - 2); q < win; ++q) mbar_wait_n(wfull0 + 8 * (q & 1), (q >> 1) & 1, 1u << 12);
+        }
+      }
+    } else {
+      // ---------------- dequantize ----------------
+      // the sets of warps that fill a stage (PAIR: 128 rows of B, 4 warps;
+      // single: 256, 8 warps) take turns
+      constexpr int WPS = PAIR ? 4 : 8, SETS = kDeqWarps / WPS;
+      const int dw = warp - 3 - C::EPI, set = dw / WPS;
+      const uint32_t lfull0 = PAIR ? map_rank(full0, 0) : full0;
+      // this thread's 128 bytes of the operand tile: FWD, row r of B; DX, row
+      // r of the step's 64 in block blk of 64 columns.  16-byte pieces are
+      // swizzled by the row, so eight lanes write eight bank groups.
+      const int r = OP == FWD ? (dw % WPS) * 32 + lane : (dw & 1) * 32 + lane;
+      const int blk = OP == FWD ? 0 : (dw % WPS) >> 1;
+      const uint32_t at = C::A_BYTES + (uint32_t)(blk * 8192 + r * 128);
+      const int swz = r & 7;
+      // its codes in a slot, its scales in a window or slot
+      const int crow = OP == FWD ? r & 127 : r, cbox = OP == FWD ? r >> 7 : blk >> 1;
+      const uint32_t codes = stage0 + C::CODE0 + (uint32_t)(cbox * C::BOX + crow * C::ROW);
+      const int cswz = C::swz(crow);
+      const uint32_t sbs = OP == FWD ? stage0 + C::WIN0 + (uint32_t)(2 * cbox * C::SB + crow * 16)
+                                     : stage0 + C::CODE0 + (uint32_t)(C::BOXES * C::BOX + crow * 16);
+      const int nwin = ((s_hi - 1) >> spw) - (s_lo >> spw) + 1;  // windows of a tile
+      const int total = my_tiles * nk;
+      const int64_t G = p.K >> p.lgs;
+      int li = set, lt = 0, n0 = 0;
+      auto settle = [&]() {  // li to a step of tile lt
+        while (li >= nk) li -= nk, ++lt;
+        n0 = lt < my_tiles ? tile_of<OP, PAIR>(p, cluster + lt * clusters).n0 : 0;
+      };
+      // first column of the unit's 64 codes and its two halves' groups
+      auto column = [&]() {
+        return OP == FWD ? (s_lo + li) * kBK : n0 + (PAIR ? 128 * (int)rank : 0) + blk * 64;
+      };
+      // scales and biases of the unit at the cursor, from global memory
+      auto fetch = [&](uint16_t (&sv)[2], uint16_t (&zv)[2]) {
+        const int i = s_lo + li, k = column();
+        int row, part;
+        if constexpr (OP == FWD) {
+          part = PAIR ? (int)rank : r >> 7;
+          row = n0 + (r & 127);
+        } else {
+          part = i >= half;
+          row = (part ? i - half : i) * kBK + r;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int kh = k + 32 * h;
+          sv[h] = zv[h] = 0;
+          if (lt < my_tiles && row < p.N && kh < p.K) {  // past the weight: zeros
+            const int64_t g = row * G + (kh >> p.lgs);
+            sv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].scales) + g);
+            zv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].biases) + g);
+          }
+        }
+      };
+      uint16_t sn[2] = {0, 0}, zn[2] = {0, 0};
+      if (total > 0) settle();
+      if (!p.sb_tma && total > 0) fetch(sn, zn);
+      int s = set % S, u = set / S, c = set % C::SLOTS, cu = set / C::SLOTS;
+      for (int j = set; j < total; j += SETS) {
+        const int i = s_lo + li, k = column();
+        uint32_t w[2][B];
+        uint16_t sv[2], zv[2];
+        if (!mbar_wait_abortable(cfull0 + 8 * c, cu & 1, kSpins, abort_flag)) *abort_flag = 1;
+        read_codes<B>(codes + (uint32_t)(c * C::SLOT), OP == FWD ? (B == 3 ? (i & 1) * 24 : 0) : (blk & 1) * 8 * B, cswz,
+                      w);
+        if (p.sb_tma) {
+          uint32_t a = sbs;
+          if constexpr (OP == FWD) {
+            const int win = lt * nwin + (i >> spw) - (s_lo >> spw);
+            if (!mbar_wait_abortable(wfull0 + 8 * (win & 1), (win >> 1) & 1, kSpins, abort_flag)) *abort_flag = 1;
+            a += (uint32_t)((win & 1) * C::WINDOW);
+          } else {
+            a += (uint32_t)(c * C::SLOT);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t o = a + (((k + 32 * h) >> p.lgs) & 7) * 2;
+            sv[h] = lds_u16(o);
+            zv[h] = lds_u16(o + C::SB);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) sv[h] = sn[h], zv[h] = zn[h];
+        }
+        li += SETS;
+        if (li >= nk) settle();
+        if (!p.sb_tma) fetch(sn, zn);
+        if (u > 0 && !mbar_wait_abortable(empty0 + 8 * s, (u - 1) & 1, kSpins, abort_flag)) *abort_flag = 1;
+        const uint32_t dst = stage0 + (uint32_t)(s * C::STAGE) + at;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          sts_v4(dst + (uint32_t)((q ^ swz) << 4), dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            arrive_remote(lfull0 + 8 * s);
+          else
+            mbar_arrive(full0 + 8 * s);
+          mbar_arrive(cempty0 + 8 * c);
+        }
+        s += SETS;
+        if (s >= S) s -= S, ++u;
+        c += SETS;
+        if (c >= C::SLOTS) c -= C::SLOTS, ++cu;
       }
     }
   }
@@ -793,8 +948,43 @@ inline bool make_map(CUtensorMap* m, const void* base, bool f16, int64_t rows, i
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The maps of the packed side of one part: codes in boxes of Cfg's shape, and
+// scales and biases in boxes of 8 groups.  False when the codes' rows do not
+// start on 16 bytes.
+template <int OP, int B>
+bool make_code_maps(Maps* tm, int part, const Args& p) {
+  using C = Cfg<OP, B, true>;
+  EncodeTiledFn enc = tensor_map_encoder();
+  const int64_t wpr = (int64_t)p.K / 32 * B, G = p.K >> p.lgs;
+  if (!enc || wpr % 4 != 0) return false;
+  const cuuint32_t estr[2] = {1, 1};
+  const cuuint64_t dims[2] = {(cuuint64_t)wpr, (cuuint64_t)p.N};
+  const cuuint64_t strides[1] = {(cuuint64_t)(wpr * 4)};
+  const cuuint32_t box[2] = {(cuuint32_t)(C::ROW / 4), (cuuint32_t)C::BOX_ROWS};
+  const CUtensorMapSwizzle swz = C::SWZ == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                 : C::SWZ == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                 : C::SWZ == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
+  if (enc(&tm->b[part], CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t*>(p.w[part].packed), dims, strides, box,
+          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  tm->s[part] = tm->z[part] = tm->b[part];
+  if (!p.sb_tma) return true;
+  const cuuint64_t gdims[2] = {(cuuint64_t)G, (cuuint64_t)p.N};
+  const cuuint64_t gstrides[1] = {(cuuint64_t)(G * 2)};
+  const cuuint32_t gbox[2] = {8, (cuuint32_t)C::BOX_ROWS};
+  for (int a = 0; a < 2; ++a)
+    if (enc(a ? &tm->z[part] : &tm->s[part], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+            const_cast<void*>(a ? p.w[part].biases : p.w[part].scales), gdims, gstrides, gbox, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
 template <int OP, int B, typename T, bool PAIR>
-cudaError_t launch(const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
+cudaError_t launch(const Args& p, const Maps& tm, int clusters, cudaStream_t st) {
   using C = Cfg<OP, B, PAIR>;
   auto k = pair_gemm_kernel<OP, B, T, PAIR>;
   static int configured[64] = {0};
@@ -820,19 +1010,23 @@ cudaError_t launch(const Args& p, const CUtensorMap (&tm)[4], int clusters, cuda
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = per > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, p, tm[0], tm[1], tm[2], tm[3]);
+  return cudaLaunchKernelEx(&cfg, k, p, tm);
 }
 
 template <int OP, int B, bool PAIR>
-cudaError_t launch_t(const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
+cudaError_t launch_t(const Args& p, const Maps& tm, int clusters, cudaStream_t st) {
   return p.f16 ? launch<OP, B, __half, PAIR>(p, tm, clusters, st)
                : launch<OP, B, __nv_bfloat16, PAIR>(p, tm, clusters, st);
 }
 
-// One bit width's kernels; DP does not depend on T.
+// One bit width's kernels; DP does not depend on T.  cudaErrorNotSupported: FWD
+// and DX want the codes' rows on 16 bytes.
 template <int B>
-cudaError_t dispatch(int op, bool pair, const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
+cudaError_t dispatch(int op, bool pair, Args& p, Maps& tm, int clusters, cudaStream_t st) {
   if (op == DP) return launch<DP, B, __nv_bfloat16, true>(p, tm, clusters, st);
+  p.sb_tma = (p.K >> p.lgs) % 8 == 0;
+  for (int i = 0; i < 2; ++i)
+    if (!(op == FWD ? make_code_maps<FWD, B>(&tm, i, p) : make_code_maps<DX, B>(&tm, i, p))) return cudaErrorNotSupported;
   if (op == FWD) return pair ? launch_t<FWD, B, true>(p, tm, clusters, st) : launch_t<FWD, B, false>(p, tm, clusters, st);
   return pair ? launch_t<DX, B, true>(p, tm, clusters, st) : launch_t<DX, B, false>(p, tm, clusters, st);
 }

@@ -4,7 +4,7 @@
 namespace qmm {
 namespace pg {
 
-cudaError_t dispatch_b8(int op, bool pair, const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
+cudaError_t dispatch_b8(int op, bool pair, Args& p, Maps& tm, int clusters, cudaStream_t st) {
   return dispatch<8>(op, pair, p, tm, clusters, st);
 }
 

@@ -79,7 +79,7 @@ static cudaError_t dequant_b(const DequantArgs& d, bool f16, dim3 grid, cudaStre
 }
 
 // Dequantizes the parts of `p` into ws, [N, K] each, and maps them for `op`.
-cudaError_t dequant_parts(int op, int bits, const Args& p, void* ws, CUtensorMap* tm, cudaStream_t st) {
+cudaError_t dequant_parts(int op, int bits, const Args& p, void* ws, Maps& tm, cudaStream_t st) {
   DequantArgs d{};
   d.rows = p.N;
   d.per_row = p.K / 8;
@@ -91,7 +91,7 @@ cudaError_t dequant_parts(int op, int bits, const Args& p, void* ws, CUtensorMap
     d.w[i] = p.w[part];
     d.out[i] = static_cast<char*>(ws) + (int64_t)part * p.N * p.K * 2;
     // FWD reads 128 rows x 64 k, DX 64 rows x 64 columns at a time
-    if (!make_map(&tm[i], d.out[i], p.f16, p.N, p.K, p.K, op == FWD ? 128 : 64)) return cudaErrorInvalidValue;
+    if (!make_map(&tm.b[i], d.out[i], p.f16, p.N, p.K, p.K, op == FWD ? 128 : 64)) return cudaErrorInvalidValue;
   }
   const int rows_per_block = 8 * (32 / d.lanes);
   const dim3 grid((unsigned)(((int64_t)p.N + rows_per_block - 1) / rows_per_block), p.parts);
@@ -104,7 +104,7 @@ cudaError_t dequant_parts(int op, int bits, const Args& p, void* ws, CUtensorMap
   }
 }
 
-cudaError_t dispatch_dense(int op, const Args& p, const CUtensorMap (&tm)[4], int clusters, cudaStream_t st) {
+cudaError_t dispatch_dense(int op, const Args& p, const Maps& tm, int clusters, cudaStream_t st) {
   return op == FWD ? launch_t<FWD, 0, true>(p, tm, clusters, st) : launch_t<DX, 0, true>(p, tm, clusters, st);
 }
 
