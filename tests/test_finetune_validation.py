@@ -61,13 +61,15 @@ def test_gate_up(L):
         return L.qmm_gate_up_silu(x, xt, M, K, ctypes.byref(g), ctypes.byref(u), h, ht, gp, up, ws, nb, None)
 
     assert call(M=0) == _lib.QMM_OK
-    assert call(M=-1) == call(K=64) == call(gp=A) == call(up=A) == call(M=9999, nb=0) == _lib.QMM_ERR_INVALID_ARG
+    assert call(M=-1) == call(K=64) == call(gp=A) == call(up=A) == _lib.QMM_ERR_INVALID_ARG
+    odd = dict(g=qw(bits=3, gs=32, cols=96), u=qw(bits=3, gs=32, cols=96), M=17, K=96)  # needs its workspace
+    assert call(**odd, nb=0) == _lib.QMM_ERR_INVALID_ARG
     for other in (qw(rows=16), qw(bits=8), qw(gs=32), qw(cols=64)):
         assert call(u=other) == _lib.QMM_ERR_INVALID_ARG
     assert call(xt=HF) == call(ht=HF) == call(u=qw(sdtype=HF)) == _lib.QMM_ERR_DTYPE
     f = qw(sdtype=F32)
     assert call(f, f, xt=F32, ht=F32) == call(mx(), mx()) == call(M=2 ** 31) == _lib.QMM_ERR_UNSUPPORTED
-    for bad in (dict(x=A + 2), dict(h=A + 8), dict(x=0), dict(M=9999, ws=A + 2), dict(M=9999, ws=None),
+    for bad in (dict(x=A + 2), dict(h=A + 8), dict(x=0), dict(odd, ws=A + 2), dict(odd, ws=None),
                 dict(gp=A + 2, up=A), dict(gp=A, up=A + 2)):
         assert call(**bad) == _lib.QMM_ERR_ALIGNMENT, bad
 
@@ -89,15 +91,15 @@ def test_backward(L):
                                            ds, dz, g, ws, nb, None)
 
     for call in (one, two):
-        for bad in (dict(M=-1), dict(K=64), dict(M=9999, nb=0), dict(dx=None, ds=None, dz=None), dict(ds=None),
+        for bad in (dict(M=-1), dict(K=64), dict(w=qw(rows=9), nb=0), dict(dx=None, ds=None, dz=None), dict(ds=None),
                     dict(dz=None), dict(w=qw(bits=7))):
             assert call(**bad) == _lib.QMM_ERR_INVALID_ARG, bad
         for bad in (dict(xt=HF), dict(g=HF), dict(g=5)):
             assert call(**bad) == _lib.QMM_ERR_DTYPE, bad
         for bad in (dict(w=mx()), dict(w=qw(sdtype=F32), xt=F32, g=F32)):
             assert call(**bad) == _lib.QMM_ERR_UNSUPPORTED, bad
-        for bad in (dict(dy=A + 2), dict(x=A + 4), dict(dx=A + 8), dict(ds=A + 2), dict(dz=A + 2), dict(M=9999, ws=A + 4),
-                    dict(M=9999, ws=None), dict(w=qw(packed=0))):
+        for bad in (dict(dy=A + 2), dict(x=A + 4), dict(dx=A + 8), dict(ds=A + 2), dict(dz=A + 2), dict(w=qw(rows=9), ws=A + 4),
+                    dict(w=qw(rows=9), ws=None), dict(w=qw(packed=0))):
             assert call(**bad) == _lib.QMM_ERR_ALIGNMENT, bad
     assert two(u=qw(rows=9)) == two(u=qw(bits=8)) == _lib.QMM_ERR_INVALID_ARG
 

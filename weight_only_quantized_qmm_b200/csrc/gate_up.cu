@@ -111,43 +111,74 @@ static pg::Args args_of(int64_t M, int64_t K, const qmm_qweight* w0, const qmm_q
   return p;
 }
 
-// bits == 0: weights dequantized beforehand
-static cudaError_t run(int op, int bits, bool pair, pg::Args& p, pg::Maps& tm, cudaStream_t st) {
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * (op == pg::DP ? p.parts : 1);
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-  int clusters = (int)std::min<int64_t>(tiles, qmm_host::num_sms() / 2);
-  p.splits = 1;
-  if (!pair) {
-    // few tiles: CTAs share a tile by cutting its sum, at least 4 steps each
-    while (p.splits < 8 && tiles * p.splits * 2 <= qmm_host::num_sms() && p.steps >= 8 * p.splits) p.splits *= 2;
-    clusters = p.splits > 1 ? (int)tiles : (int)std::min<int64_t>(tiles, qmm_host::num_sms());
+static int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// How a product runs: weights dequantized beforehand or in the kernel, on CTA
+// pairs or single CTAs, and how many of those share a tile.
+struct Plan {
+  bool dense, pair;
+  int splits;
+  int m_tiles, n_tiles;
+};
+
+// The cheapest by the times measured for one 64-deep step (us, 4096 x 14336): a
+// pair's 256 x 256 tile 0.29 from dense weights and 0.34 dequantizing, a
+// single CTA's 128 x 256 tile 0.62; 2 us to join splits; and for the
+// dequantizing pass 2 us and its bytes at 4.5 TB/s.  Kernels that dequantize want
+// rows of codes on 16 bytes.  A cluster of 8 CTAs finds room on 128 SMs, one of 4
+// on 144.
+static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits) {
+  const int64_t out = op == pg::FWD ? N : K;  // columns of the output
+  const int tn = op == pg::FWD ? 128 : 256;
+  const int steps = op == pg::FWD ? ceil_div(K, pg::kBK) : parts * ceil_div(N, pg::kBK);
+  const int sms = qmm_host::num_sms();
+  Plan best{};
+  double cost = 1e300;
+  for (int kind = 0; kind < 3; ++kind) {
+    const bool dense = kind == 0, pair = kind < 2;
+    if (!dense && (K * bits) % 128 != 0) continue;
+    const int64_t mt = ceil_div(M, pair ? 256 : 128), nt = ceil_div(out, tn);
+    for (int s = 1; s <= (pair ? 4 : 8); s *= 2) {
+      const int ctas = (pair ? 2 : 1) * s;
+      const int room = (ctas >= 8 ? sms * 128 / 148 : ctas >= 4 ? sms * 144 / 148 : sms) / ctas;
+      if (s > 1 && (mt * nt > room || steps < 4 * s)) break;
+      const double waves = (double)((mt * nt + room - 1) / room);
+      const double c = waves * ceil_div(steps, s) * (dense ? 0.29 : pair ? 0.34 : 0.62) + (s > 1 ? 2.0 : 0.0) +
+                       (dense ? 2.0 + (double)parts * N * K * (2.0 + bits / 8.0) / 4.5e6 : 0.0);
+      if (c < cost) {
+        cost = c;
+        best = Plan{dense, pair, s, (int)mt, (int)nt};
+      }
+    }
   }
+  return best;
+}
+
+// bits == 0: weights dequantized beforehand
+static cudaError_t run(int op, int bits, const Plan& plan, pg::Args& p, pg::Maps& tm, cudaStream_t st) {
+  p.m_tiles = plan.m_tiles;
+  p.n_tiles = plan.n_tiles;
+  p.splits = plan.splits;
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * (op == pg::DP ? p.parts : 1);
+  if (tiles > INT32_MAX / 16) return cudaErrorInvalidValue;
+  const int sms = qmm_host::num_sms();
+  const int clusters = plan.splits > 1 ? (int)tiles : (int)std::min<int64_t>(tiles, plan.pair ? sms / 2 : sms);
   switch (bits) {
     case 0: return pg::dispatch_dense(op, p, tm, clusters, st);
-    case 2: return pg::dispatch_b2(op, pair, p, tm, clusters, st);
-    case 3: return pg::dispatch_b3(op, pair, p, tm, clusters, st);
-    case 4: return pg::dispatch_b4(op, pair, p, tm, clusters, st);
-    case 6: return pg::dispatch_b6(op, pair, p, tm, clusters, st);
-    default: return pg::dispatch_b8(op, pair, p, tm, clusters, st);
+    case 2: return pg::dispatch_b2(op, plan.pair, p, tm, clusters, st);
+    case 3: return pg::dispatch_b3(op, plan.pair, p, tm, clusters, st);
+    case 4: return pg::dispatch_b4(op, plan.pair, p, tm, clusters, st);
+    case 6: return pg::dispatch_b6(op, plan.pair, p, tm, clusters, st);
+    default: return pg::dispatch_b8(op, plan.pair, p, tm, clusters, st);
   }
 }
 
-static int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-// Whether the weights are dequantized into the workspace first: the pass costs
-// about 60 us for gate and up of 4096 x 14336, and the product then runs at
-// 1375 TFLOP/s instead of 1070 (measured at 4096 and 1024 tokens).
-// The kernels that dequantize themselves want rows of codes on 16 bytes.
-static bool dense_first(int64_t M, int64_t K, int bits) { return M >= 1536 || (K * bits) % 128 != 0; }
-
-// dense: room for both dequantized weights, or null
+// dense: room for both dequantized weights where the plan wants it
 static cudaError_t forward(const void* x, int x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
                            const qmm_qweight* up, void* h, int h_dtype, void* gp, void* upre, void* dense,
                            cudaStream_t st) {
   pg::Args p = args_of(M, K, gate, up, x_dtype);
-  const bool pair = dense || M > 128;
-  p.m_tiles = ceil_div(M, pair ? 256 : 128);
-  p.n_tiles = ceil_div(p.N, 128);
+  const Plan plan = plan_of(pg::FWD, M, K, gate->rows, 2, gate->bits);
   p.steps = ceil_div(K, pg::kBK);
   p.out[0] = h;
   p.out[1] = gp;
@@ -156,11 +187,8 @@ static cudaError_t forward(const void* x, int x_dtype, int64_t M, int64_t K, con
   pg::Maps tm;
   if (!pg::make_map(&tm.a[0], x, p.f16, M, K, K, 128)) return cudaErrorInvalidValue;
   tm.a[1] = tm.b[0] = tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.a[0];
-  if (dense) {
-    const cudaError_t e = pg::dequant_parts(pg::FWD, gate->bits, p, dense, tm, st);
-    return e != cudaSuccess ? e : run(pg::FWD, 0, true, p, tm, st);
-  }
-  return run(pg::FWD, gate->bits, pair, p, tm, st);
+  const cudaError_t e = plan.dense ? pg::dequant_parts(pg::FWD, gate->bits, p, dense, tm, st) : cudaSuccess;
+  return e != cudaSuccess ? e : run(pg::FWD, plan.dense ? 0 : gate->bits, plan, p, tm, st);
 }
 
 // dy0 (and dy1): [M, N] in rows of ld elements, ld a multiple of 8
@@ -178,23 +206,20 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
   pg::Maps tm;
   if (dx) {
     pg::Args p = args_of(M, K, w0, w1, x_dtype);
-    const bool pair = dense || M > 128;
-    p.m_tiles = ceil_div(M, pair ? 256 : 128);
-    p.n_tiles = ceil_div(K, 256);
+    const Plan plan = plan_of(pg::DX, M, K, N, p.parts, w0->bits);
     p.steps = p.parts * ceil_div(N, pg::kBK);
     p.out[0] = dx;
     p.out_dtype = x_dtype;
     if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 128) || !pg::make_map(&tm.a[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 128))
       return cudaErrorInvalidValue;
     tm.b[0] = tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.a[0];
-    cudaError_t e = dense ? pg::dequant_parts(pg::DX, w0->bits, p, dense, tm, st) : cudaSuccess;
-    if (e == cudaSuccess) e = run(pg::DX, dense ? 0 : w0->bits, pair, p, tm, st);
+    cudaError_t e = plan.dense ? pg::dequant_parts(pg::DX, w0->bits, p, dense, tm, st) : cudaSuccess;
+    if (e == cudaSuccess) e = run(pg::DX, plan.dense ? 0 : w0->bits, plan, p, tm, st);
     if (e != cudaSuccess) return e;
   }
   if (grads[0]) {
     pg::Args p = args_of(M, K, w0, w1, x_dtype);
-    p.m_tiles = ceil_div(N, 256);
-    p.n_tiles = ceil_div(K, 256);
+    const Plan plan{true, true, 1, ceil_div(N, 256), ceil_div(K, 256)};
     p.steps = ceil_div(M, pg::kBK);
     for (int i = 0; i < 4; ++i) p.out[i] = grads[i];
     p.out_dtype = g_dtype;
@@ -202,16 +227,16 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
         !pg::make_map(&tm.b[0], x, p.f16, M, K, K, 64))
       return cudaErrorInvalidValue;
     tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.b[0];
-    return run(pg::DP, w0->bits, true, p, tm, st);
+    return run(pg::DP, w0->bits, plan, p, tm, st);
   }
   return cudaSuccess;
 }
 
 static int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
 static int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
-// bytes of `parts` dequantized weights for M tokens
-static int64_t dense_bytes(int64_t M, int64_t K, int64_t N, int bits, int parts) {
-  return dense_first(M, K, bits) ? parts * N * K * 2 : 0;
+// bytes of the weights that the plan wants dequantized
+static int64_t dense_bytes(int op, int64_t M, int64_t K, int64_t N, int bits, int parts) {
+  return M > 0 && N > 0 && plan_of(op, M, K, N, parts, bits).dense ? parts * N * K * 2 : 0;
 }
 
 }  // namespace ffn
@@ -257,7 +282,7 @@ extern "C" {
 
 int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits) {
   if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F) || qmm_packed_words_per_row(K, bits) < 0) return -1;
-  return M > kFewTokens ? qmm::ffn::dense_bytes(M, K, F, bits, 2) : 0;
+  return M > kFewTokens ? qmm::ffn::dense_bytes(qmm::pg::FWD, M, K, F, bits, 2) : 0;
 }
 
 qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
@@ -280,14 +305,14 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
     const cudaError_t e = qmm::launch_qgemv(p, gate->bits, gate->group_size, x_dtype, true, st);
     return e == cudaErrorInvalidValue ? QMM_ERR_UNSUPPORTED : launch_status(e);
   }
-  return launch_status(qmm::ffn::forward(x, x_dtype, M, K, gate, up, h, h_dtype, g_pre, u_pre,
-                                         need > 0 ? workspace : nullptr, st));
+  return launch_status(qmm::ffn::forward(x, x_dtype, M, K, gate, up, h, h_dtype, g_pre, u_pre, workspace, st));
 }
 
 int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits) {
   if (!i32(M) || !i32(K) || !i32(N) || !fits(M, K, N) || qmm_packed_words_per_row(K, bits) < 0) return -1;
   // rows of dy that do not start on 16 bytes are copied to ones that do
-  return qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) + qmm::ffn::dense_bytes(M, K, N, bits, 1);
+  return qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) + 
+         qmm::ffn::dense_bytes(qmm::pg::DX, M, K, N, bits, 1);
 }
 
 qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype, int64_t M, int64_t K,
@@ -315,13 +340,14 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
     if (e != cudaSuccess) return launch_status(e);
     dy = workspace;
   }
-  void* dense = qmm::ffn::dense_first(M, K, w->bits) ? static_cast<char*>(workspace) + qmm::ffn::align16(N % 8 ? M * ld * 2 : 0) : nullptr;
+  void* dense = static_cast<char*>(workspace) + qmm::ffn::align16(N % 8 ? M * ld * 2 : 0);
   return launch_status(qmm::ffn::backward(dy, nullptr, ld, x, x_dtype, M, K, w, nullptr, dx, grads, g_dtype, dense, st));
 }
 
 int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits) {
   if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F) || qmm_packed_words_per_row(K, bits) < 0) return -1;
-  return qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) + qmm::ffn::dense_bytes(M, K, F, bits, 2);  // dg and du first
+  return qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) + 
+         qmm::ffn::dense_bytes(qmm::pg::DX, M, K, F, bits, 2);  // dg and du first
 }
 
 qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* g_pre, const void* u_pre,
@@ -357,7 +383,7 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
             : qmm::ffn::act_grad<__half>(dh, g_pre, u_pre, n, (int)F, (int)ld, dg, du, st);
     if (e != cudaSuccess) return launch_status(e);
   }
-  void* dense = qmm::ffn::dense_first(M, K, gate->bits) ? static_cast<char*>(workspace) + qmm::ffn::align16(2 * M * ld * 2) : nullptr;
+  void* dense = static_cast<char*>(workspace) + qmm::ffn::align16(2 * M * ld * 2);
   return launch_status(qmm::ffn::backward(dg, du, ld, x, x_dtype, M, K, gate, up, dx, grads, g_dtype, dense, st));
 }
 

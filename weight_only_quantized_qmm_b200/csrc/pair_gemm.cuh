@@ -17,8 +17,9 @@
 // of A and half of B, so an SM reads and writes 64 KB of shared memory per
 // 64-deep step (512 tensor cycles) instead of the 96 KB of a 128 x 256 tile,
 // which is what bounds that tile.  Single: one CTA per 128 x 256 tile for few
-// tokens; a cluster of `splits` CTAs may share a tile by cutting the sum, and
-// joins its partial tiles through distributed shared memory in rank order.
+// tokens.  Where the tiles are few, a cluster of `splits` CTAs (or pairs) shares
+// one by cutting the sum, and joins its partial tiles through distributed shared
+// memory in rank order.
 //
 // FWD and DX take weights dequantized beforehand (B = 0: many tokens, where the
 // extra pass is small beside the product and the two TMA-fed operands run at
@@ -57,7 +58,6 @@ enum Op { FWD = 0, DX = 1, DP = 2 };
 constexpr int kBK = 64;                  // depth of a step: 128 bytes of 16-bit values
 constexpr int kTile = 128 * kBK * 2;     // 128 x 64 operand tile: 16 KB
 constexpr int kDeqWarps = 16;
-constexpr uint32_t kSpins = 1u << 22;
 
 // The widths of FWD and DX, with B = 0 for weights dequantized beforehand.
 template <int OP, int B, bool PAIR>
@@ -95,7 +95,7 @@ struct Cfg {
   static_assert(DENSE || SLOTS >= 3, "room for the codes");
   static_assert(8 * BARS + 8 <= 512, "barriers, TMEM slot and abort flag");
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(PAIR || 128 * 256 * 4 <= CODE0, "a partial tile fits the stages");
+  static_assert(128 * 256 * 4 <= CODE0, "a partial tile fits the stages");
   __device__ static constexpr int swz(int r) {
     return SWZ == 32 ? (r >> 2) & 1 : SWZ == 64 ? (r >> 1) & 3 : SWZ == 128 ? r & 7 : 0;
   }
@@ -114,7 +114,7 @@ struct Args {
   int lgs;                // log2 of the group size
   int m_tiles, n_tiles;   // tiles along the output's rows and columns (DP: rows of one part)
   int steps;              // 64-deep steps of the whole sum
-  int splits;             // CTAs that share a tile by cutting the sum (single)
+  int splits;             // CTAs (PAIR: pairs) that share a tile by cutting the sum; 1: persistent
   void* out[4];           // FWD: h, g, u; DX: dx; DP: dscales, dbiases of both parts
   int out_dtype;          // FWD: of h; DP
   int f16;                // operands are f16 (otherwise bf16)
@@ -150,21 +150,52 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// as mbar_wait_abortable, acquiring what the other CTA of the pair released
+// Bounded waits of this kernel: polls that may sleep up to kNap ns each (a
+// waiting warp that polls without a nap takes issue slots from the dequant
+// warps), giving up after kPolls of them or when another role has raised the
+// abort flag.
+constexpr uint32_t kNap = 20000, kPolls = 1u << 17;
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(kNap)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const int* abort_flag) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    if (poll(bar, parity)) return true;
+    if (*reinterpret_cast<const volatile int*>(abort_flag)) return false;
+  }
+  return false;
+}
+// the same, acquiring what the other CTA of the pair released
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const int* abort_flag) {
-  for (uint32_t i = 0; i < kSpins; ++i) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(kNap)
         : "memory");
     if (done) return true;
-    if ((i & 1023u) == 1023u && *reinterpret_cast<const volatile int*>(abort_flag)) return false;
+    if (*reinterpret_cast<const volatile int*>(abort_flag)) return false;
   }
   return false;
+}
+// One poll is the usual case; the full bounded wait stands aside, and one that
+// gives up raises the abort flag.
+static __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, int* abort_flag) {
+  if (!wait(bar, parity, abort_flag)) *abort_flag = 1;
+}
+__device__ __forceinline__ void wait_fast(uint32_t bar, uint32_t parity, int* abort_flag) {
+  if (!poll(bar, parity)) wait_slow(bar, parity, abort_flag);
 }
 template <bool PAIR>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
@@ -209,11 +240,11 @@ __device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t a, uint64_t b, uin
 }
 // arrives on `bar` (PAIR: of both CTAs) once the MMAs issued so far are done
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
   if constexpr (PAIR)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << lead))
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -406,7 +437,7 @@ __device__ __forceinline__ void store_h8(const Args& p, int m, int n, const floa
   const int64_t at = (int64_t)m * p.N + n;
   float h[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
+  for (int i = 0; i < 8; ++i) h[i] = g[i] * __fdividef(1.0f, 1.0f + __expf(-g[i])) * u[i];  // within 2^-19
   if (p.out_dtype == QMM_F32)
     store8(reinterpret_cast<float*>(p.out[0]) + at, h, vec, cnt);
   else
@@ -438,11 +469,13 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
-  const bool leader = !PAIR || rank == 0;
-  const int splits = PAIR ? 1 : p.splits;
-  const int cta_per = PAIR ? 2 : splits;  // CTAs of a cluster
+  const int side = PAIR ? (int)(rank & 1u) : 0;        // this CTA's half of the pair's tile
+  const uint32_t lead = PAIR ? rank & ~1u : rank;      // rank of the pair's leader
+  const bool leader = side == 0;
+  const int splits = p.splits;
+  const int cta_per = (PAIR ? 2 : 1) * splits;  // CTAs of a cluster
   const int cluster = blockIdx.x / cta_per, clusters = gridDim.x / cta_per;
-  const int split = PAIR ? 0 : (int)rank;
+  const int split = PAIR ? (int)(rank >> 1) : (int)rank;
   // this CTA's range of steps, and its cluster's tiles
   const int s_lo = (int)((int64_t)p.steps * split / splits), s_hi = (int)((int64_t)p.steps * (split + 1) / splits);
   const int nk = s_hi - s_lo;
@@ -492,15 +525,15 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       constexpr uint32_t kTx = (PAIR ? 2 : 1) * (C::DENSE ? C::STAGE : C::A_BYTES);
-      const uint32_t lfull0 = PAIR ? map_rank(full0, 0) : full0;
+      const uint32_t lfull0 = PAIR ? map_rank(full0, lead) : full0;
       const int half = OP == DP ? 0 : p.steps / p.parts;  // DX: steps of one part
       int s = 0, u = 0, issued = 0;
       bool stop = false;
       for (int lt = 0; lt < my_tiles && !stop; ++lt) {
         const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
-        const int row = tl.m0 + (PAIR ? 128 * (int)rank : 0);
+        const int row = tl.m0 + 128 * side;
         for (int i = s_lo; i < s_hi; ++i) {
-          if (u > 0 && !mbar_wait_abortable(empty0 + 8 * s, (u - 1) & 1, kSpins, abort_flag)) {
+          if (u > 0 && !wait(empty0 + 8 * s, (u - 1) & 1, abort_flag)) {
             *abort_flag = 1;
             stop = true;
             break;
@@ -509,7 +542,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
           if (leader) mbar_arrive_expect_tx(full0 + 8 * s, kTx);
           if constexpr (OP == DP) {
             const CUtensorMap* ma = &tm.a[tl.part];
-            const int col = tl.n0 + 128 * (int)rank;
+            const int col = tl.n0 + 128 * side;
             tma_2d<PAIR>(a, ma, row, i * kBK, bar);
             tma_2d<PAIR>(a + 8192, ma, row + 64, i * kBK, bar);
             tma_2d<PAIR>(a + C::A_BYTES, &tm.b[0], col, i * kBK, bar);
@@ -520,13 +553,13 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
             tma_2d<PAIR>(a, &tm.a[second], n, row, bar);
             if constexpr (C::DENSE) {
               const CUtensorMap* mb = &tm.b[second];
-              const int col = tl.n0 + 128 * (int)rank;
+              const int col = tl.n0 + 128 * side;
               tma_2d<PAIR>(a + C::A_BYTES, mb, col, n, bar);
               tma_2d<PAIR>(a + C::A_BYTES + 8192, mb, col + 64, n, bar);
             }
           } else {
             tma_2d<PAIR>(a, &tm.a[0], i * kBK, row, bar);
-            if constexpr (C::DENSE) tma_2d<PAIR>(a + C::A_BYTES, &tm.b[rank], i * kBK, tl.n0, bar);
+            if constexpr (C::DENSE) tma_2d<PAIR>(a + C::A_BYTES, &tm.b[side], i * kBK, tl.n0, bar);
           }
           ++issued;
           if (++s == S) s = 0, ++u;
@@ -573,34 +606,223 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
             mma<PAIR>(acc, desc<AMN>(a0 + kk * AK), desc<BMN>(b0 + kk * BK_), idesc, (i | kk) != 0 ? 1u : 0u);
-          commit<PAIR>(empty0 + 8 * s);
+          commit<PAIR>(empty0 + 8 * s, lead);
           if (++s == S) s = 0, ++u;
         }
-        commit<PAIR>(accf0 + 8 * b);  // (also after a failure)
+        commit<PAIR>(accf0 + 8 * b, lead);  // (also after a failure)
       }
       // TMEM is released only once every issued MMA is done
-      commit<PAIR>(drain);
-      mbar_wait_n(drain, 0, kSpins);
+      commit<PAIR>(drain, lead);
+      for (uint32_t i = 0; i < kPolls && !poll(drain, 0); ++i) {
+      }
     }
-  } else if (warp < 2 + C::EPI) {
-    // ---------------- epilogue ----------------
+  } else if (!C::DENSE && warp >= 2 + C::EPI) {
+   if constexpr (!C::DENSE) {
+    const int half = p.steps / p.parts;    // DX: steps of one part
+    const int spw = p.lgs - 3;             // log2 of the steps of a window: 8 groups
+    if (warp == 2 + C::EPI) {
+      // ---------------- producer of the codes, scales and biases ----------------
+      if (lane == 0) {
+        const uint32_t sb_tx = p.sb_tma ? 2 * C::SB : 0;
+        int j = 0, done = 0, win = 0, win_start = 0;  // done: steps known to be dequantized
+        bool stop = false;
+        auto reach = [&](int upto) {
+          for (; done < upto; ++done)
+            if (!wait(cempty0 + 8 * (done % C::SLOTS), (done / C::SLOTS) & 1, abort_flag))
+              return false;
+          return true;
+        };
+        for (int lt = 0; lt < my_tiles && !stop; ++lt) {
+          const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
+          for (int i = s_lo; i < s_hi; ++i, ++j) {
+            if (OP == FWD && p.sb_tma && (i == s_lo || (i & ((1 << spw) - 1)) == 0)) {
+              // the window before the last one makes room
+              if (!reach(win_start)) {
+                stop = true;
+                break;
+              }
+              const uint32_t d = stage0 + C::WIN0 + (win & 1) * C::WINDOW, bar = wfull0 + 8 * (win & 1);
+              const int g = ((i * kBK) >> p.lgs) & ~7;
+              mbar_arrive_expect_tx(bar, C::WINDOW);
+#pragma unroll
+              for (int x = 0; x < C::BOXES; ++x) {
+                const int part = PAIR ? side : x;
+                tma_2d<false>(d + (2 * x) * C::SB, &tm.s[part], g, tl.n0, bar);
+                tma_2d<false>(d + (2 * x + 1) * C::SB, &tm.z[part], g, tl.n0, bar);
+              }
+              ++win;
+              win_start = j;
+            }
+            if (!reach(j - C::SLOTS + 1)) {
+              stop = true;
+              break;
+            }
+            const uint32_t d = stage0 + C::CODE0 + (j % C::SLOTS) * C::SLOT, bar = cfull0 + 8 * (j % C::SLOTS);
+            mbar_arrive_expect_tx(bar, C::BOXES * C::BOX + (OP == DX ? sb_tx : 0u));
+            if constexpr (OP == FWD) {
+              const int w = B == 3 ? (i >> 1) * 12 : i * 2 * B;  // first word
+#pragma unroll
+              for (int x = 0; x < C::BOXES; ++x)
+                tma_2d<false>(d + x * C::BOX, &tm.b[PAIR ? side : x], w, tl.n0, bar);
+            } else {
+              const int part = i >= half, n = (part ? i - half : i) * kBK;
+              const int col = tl.n0 + 128 * side;
+#pragma unroll
+              for (int x = 0; x < C::BOXES; ++x)
+                tma_2d<false>(d + x * C::BOX, &tm.b[part], ((col + 128 * x) >> 5) * B, n, bar);
+              if (p.sb_tma) {
+                const int g = (col >> p.lgs) & ~7;
+                tma_2d<false>(d + C::BOXES * C::BOX, &tm.s[part], g, n, bar);
+                tma_2d<false>(d + C::BOXES * C::BOX + C::SB, &tm.z[part], g, n, bar);
+              }
+            }
+          }
+        }
+        if (stop) {
+          // (as the other producer: copies may be landing)
+          *abort_flag = 1;
+          for (int q = max(0, j - C::SLOTS); q < j; ++q)
+            mbar_wait_n(cfull0 + 8 * (q % C::SLOTS), (q / C::SLOTS) & 1, 1u << 12);
+          for (int q = max(0, win - 2); q < win; ++q) mbar_wait_n(wfull0 + 8 * (q & 1), (q >> 1) & 1, 1u << 12);
+        }
+      }
+    } else {
+      // ---------------- dequantize ----------------
+      // the sets of warps that fill a stage (PAIR: 128 rows of B, 4 warps;
+      // single: 256, 8 warps) take turns
+      constexpr int WPS = PAIR ? 4 : 8, SETS = kDeqWarps / WPS;
+      const int dw = warp - 3 - C::EPI, set = dw / WPS;
+      const uint32_t lfull0 = PAIR ? map_rank(full0, lead) : full0;
+      // this thread's 128 bytes of the operand tile: FWD, row r of B; DX, row
+      // r of the step's 64 in block blk of 64 columns.  16-byte pieces are
+      // swizzled by the row, so eight lanes write eight bank groups.
+      const int r = OP == FWD ? (dw % WPS) * 32 + lane : (dw & 1) * 32 + lane;
+      const int blk = OP == FWD ? 0 : (dw % WPS) >> 1;
+      const uint32_t at = C::A_BYTES + (uint32_t)(blk * 8192 + r * 128);
+      const int swz = r & 7;
+      // its codes in a slot, its scales in a window or slot
+      const int crow = OP == FWD ? r & 127 : r, cbox = OP == FWD ? r >> 7 : blk >> 1;
+      const uint32_t codes = stage0 + C::CODE0 + (uint32_t)(cbox * C::BOX + crow * C::ROW);
+      const int cswz = C::swz(crow);
+      const uint32_t sbs = OP == FWD ? stage0 + C::WIN0 + (uint32_t)(2 * cbox * C::SB + crow * 16)
+                                     : stage0 + C::CODE0 + (uint32_t)(C::BOXES * C::BOX + crow * 16);
+      const int nwin = ((s_hi - 1) >> spw) - (s_lo >> spw) + 1;  // windows of a tile
+      const int total = my_tiles * nk;
+      const int64_t G = p.K >> p.lgs;
+      int li = set, lt = 0, n0 = 0;
+      auto settle = [&]() {  // li to a step of tile lt
+        while (li >= nk) li -= nk, ++lt;
+        n0 = lt < my_tiles ? tile_of<OP, PAIR>(p, cluster + lt * clusters).n0 : 0;
+      };
+      // first column of the unit's 64 codes and its two halves' groups
+      auto column = [&]() {
+        return OP == FWD ? (s_lo + li) * kBK : n0 + 128 * side + blk * 64;
+      };
+      // scales and biases of the unit at the cursor, from global memory
+      auto fetch = [&](uint16_t (&sv)[2], uint16_t (&zv)[2]) {
+        const int i = s_lo + li, k = column();
+        int row, part;
+        if constexpr (OP == FWD) {
+          part = PAIR ? side : r >> 7;
+          row = n0 + (r & 127);
+        } else {
+          part = i >= half;
+          row = (part ? i - half : i) * kBK + r;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int kh = k + 32 * h;
+          sv[h] = zv[h] = 0;
+          if (lt < my_tiles && row < p.N && kh < p.K) {  // past the weight: zeros
+            const int64_t g = row * G + (kh >> p.lgs);
+            sv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].scales) + g);
+            zv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].biases) + g);
+          }
+        }
+      };
+      uint16_t sn[2] = {0, 0}, zn[2] = {0, 0};
+      if (total > 0) settle();
+      if (!p.sb_tma && total > 0) fetch(sn, zn);
+      int s = set % S, u = set / S, c = set % C::SLOTS, cu = set / C::SLOTS;
+      uint32_t dst = stage0 + (uint32_t)(s * C::STAGE) + at + (uint32_t)(swz << 4);
+      uint32_t src = codes + (uint32_t)(c * C::SLOT);
+      int win_in = -1;  // FWD: the last window waited for
+      for (int j = set; j < total; j += SETS) {
+        const int i = s_lo + li, k = column();
+        uint32_t w[2][B];
+        uint16_t sv[2], zv[2];
+        wait_fast(cfull0 + 8 * c, cu & 1, abort_flag);
+        read_codes<B>(src, OP == FWD ? (B == 3 ? (i & 1) * 24 : 0) : (blk & 1) * 8 * B, cswz, w);
+        if (p.sb_tma) {
+          uint32_t o = sbs + ((k >> p.lgs) & 7) * 2;
+          if constexpr (OP == FWD) {
+            const int win = lt * nwin + (i >> spw) - (s_lo >> spw);
+            if (win != win_in) wait_fast(wfull0 + 8 * (win & 1), (win >> 1) & 1, abort_flag);
+            win_in = win;
+            o += (uint32_t)((win & 1) * C::WINDOW);
+          } else {
+            o += (uint32_t)(c * C::SLOT);
+          }
+          sv[0] = sv[1] = lds_u16(o);
+          zv[0] = zv[1] = lds_u16(o + C::SB);
+          if (p.lgs == 5) {  // 64 codes are two groups
+            sv[1] = lds_u16(o + 2);
+            zv[1] = lds_u16(o + C::SB + 2);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) sv[h] = sn[h], zv[h] = zn[h];
+        }
+        li += SETS;
+        if (li >= nk) settle();
+        if (!p.sb_tma) fetch(sn, zn);
+        if (u > 0) wait_fast(empty0 + 8 * s, (u - 1) & 1, abort_flag);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          sts_v4(dst ^ (uint32_t)(q << 4), dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            arrive_remote(lfull0 + 8 * s);
+          else
+            mbar_arrive(full0 + 8 * s);
+          mbar_arrive(cempty0 + 8 * c);
+        }
+        s += SETS, dst += SETS * C::STAGE;
+        if (s >= S) s -= S, ++u, dst -= S * C::STAGE;
+        c += SETS, src += SETS * C::SLOT;
+        if (c >= C::SLOTS) c -= C::SLOTS, ++cu, src -= C::SLOTS * C::SLOT;
+      }
+    }
+   }
+  }
+
+  // ---------------- epilogue ----------------
+  // The epilogue warps; where each CTA has one tile, the dequant warps too once
+  // they are done (a tile's columns are dealt out 16 at a time).
+  const bool only = T_all <= clusters;
+  if ((warp >= 2 && warp < 2 + C::EPI) || (!C::DENSE && only && warp > 2 + C::EPI)) {
+    constexpr int kEach = C::EPI / 4 + C::DEQ / 4;  // warps of a lane quarter, when all take part
+    const int first = (C::DENSE || !only || warp < 2 + C::EPI) ? 0 : 16 * (1 + (warp - 3 - C::EPI) / 4);
+    const int stride = (C::DENSE || !only) ? 16 : 16 * kEach;
     const int qq = warp & 3;           // the TMEM lanes this warp may read
     const int r = qq * 32 + lane;      // row of the CTA's 128
     const uint32_t lanes = tmem + ((uint32_t)(qq * 32) << 16);
-    const uint32_t ltfree0 = PAIR ? map_rank(tfree0, 0) : tfree0;
+    const uint32_t ltfree0 = PAIR ? map_rank(tfree0, lead) : tfree0;
     const float nan = __int_as_float(0x7fc00000);
     bool failed = false;
     for (int lt = 0; lt < my_tiles; ++lt) {
       const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
       const int b = lt & 1;
       if (!failed) {
-        failed = !mbar_wait_abortable(accf0 + 8 * b, (lt >> 1) & 1, kSpins, abort_flag) ||
+        failed = !wait(accf0 + 8 * b, (lt >> 1) & 1, abort_flag) ||
                  *reinterpret_cast<volatile int*>(abort_flag);
         failed = __any_sync(0xffffffffu, failed);
       }
       fence_after();
       const uint32_t acc = lanes + (uint32_t)(b * 256);
-      const int row = tl.m0 + (PAIR ? 128 * (int)rank : 0) + r;
+      const int row = tl.m0 + 128 * side + r;
       if constexpr (OP == DP) {
         // 128 columns of one weight row: units of 32, groups of 1, 2 or 4
         const int c0 = ((warp - 2) >> 2) * 128;
@@ -647,10 +869,10 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
             }
           }
         }
-      } else if (!PAIR && splits > 1) {
+      } else if (splits > 1) {
         // a partial tile: four columns of all 128 rows are 2 KB
 #pragma unroll 1
-        for (int c = 0; c < 256; c += 16) {
+        for (int c = first; c < 256; c += stride) {
           float v[16];
           if (!failed) {
             tmem_ld16(acc + (uint32_t)c, v);
@@ -668,7 +890,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
       } else if constexpr (OP == FWD) {
         const bool vec = p.N % 8 == 0;
 #pragma unroll 1
-        for (int c = 0; c < 128 && tl.n0 + c < p.N; c += 16) {
+        for (int c = first; c < 128 && tl.n0 + c < p.N; c += stride) {
           float g[16], u[16];
           if (!failed) {
             tmem_ld16(acc + (uint32_t)c, g);
@@ -685,7 +907,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < 256 && tl.n0 + c < p.K; c += 16) {
+        for (int c = first; c < 256 && tl.n0 + c < p.K; c += stride) {
           float v[16];
           if (!failed) {
             tmem_ld16(acc + (uint32_t)c, v);
@@ -703,205 +925,29 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
       }
       fence_before();
       __syncwarp();
-      if (lane == 0 && !failed) {
+      if (lane == 0 && !failed && warp < 2 + C::EPI) {
         if constexpr (PAIR)
           arrive_remote(ltfree0 + 8 * b);
         else
           mbar_arrive(tfree0 + 8 * b);
       }
     }
-  } else if constexpr (!C::DENSE) {
-    const int half = p.steps / p.parts;    // DX: steps of one part
-    const int spw = p.lgs - 3;             // log2 of the steps of a window: 8 groups
-    if (warp == 2 + C::EPI) {
-      // ---------------- producer of the codes, scales and biases ----------------
-      if (lane == 0) {
-        const uint32_t sb_tx = p.sb_tma ? 2 * C::SB : 0;
-        int j = 0, done = 0, win = 0, win_start = 0;  // done: steps known to be dequantized
-        bool stop = false;
-        auto reach = [&](int upto) {
-          for (; done < upto; ++done)
-            if (!mbar_wait_abortable(cempty0 + 8 * (done % C::SLOTS), (done / C::SLOTS) & 1, kSpins, abort_flag))
-              return false;
-          return true;
-        };
-        for (int lt = 0; lt < my_tiles && !stop; ++lt) {
-          const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
-          for (int i = s_lo; i < s_hi; ++i, ++j) {
-            if (OP == FWD && p.sb_tma && (i == s_lo || (i & ((1 << spw) - 1)) == 0)) {
-              // the window before the last one makes room
-              if (!reach(win_start)) {
-                stop = true;
-                break;
-              }
-              const uint32_t d = stage0 + C::WIN0 + (win & 1) * C::WINDOW, bar = wfull0 + 8 * (win & 1);
-              const int g = ((i * kBK) >> p.lgs) & ~7;
-              mbar_arrive_expect_tx(bar, C::WINDOW);
-#pragma unroll
-              for (int x = 0; x < C::BOXES; ++x) {
-                const int part = PAIR ? (int)rank : x;
-                tma_2d<false>(d + (2 * x) * C::SB, &tm.s[part], g, tl.n0, bar);
-                tma_2d<false>(d + (2 * x + 1) * C::SB, &tm.z[part], g, tl.n0, bar);
-              }
-              ++win;
-              win_start = j;
-            }
-            if (!reach(j - C::SLOTS + 1)) {
-              stop = true;
-              break;
-            }
-            const uint32_t d = stage0 + C::CODE0 + (j % C::SLOTS) * C::SLOT, bar = cfull0 + 8 * (j % C::SLOTS);
-            mbar_arrive_expect_tx(bar, C::BOXES * C::BOX + (OP == DX ? sb_tx : 0u));
-            if constexpr (OP == FWD) {
-              const int w = B == 3 ? (i >> 1) * 12 : i * 2 * B;  // first word
-#pragma unroll
-              for (int x = 0; x < C::BOXES; ++x)
-                tma_2d<false>(d + x * C::BOX, &tm.b[PAIR ? (int)rank : x], w, tl.n0, bar);
-            } else {
-              const int part = i >= half, n = (part ? i - half : i) * kBK;
-              const int col = tl.n0 + (PAIR ? 128 * (int)rank : 0);
-#pragma unroll
-              for (int x = 0; x < C::BOXES; ++x)
-                tma_2d<false>(d + x * C::BOX, &tm.b[part], ((col + 128 * x) >> 5) * B, n, bar);
-              if (p.sb_tma) {
-                const int g = (col >> p.lgs) & ~7;
-                tma_2d<false>(d + C::BOXES * C::BOX, &tm.s[part], g, n, bar);
-                tma_2d<false>(d + C::BOXES * C::BOX + C::SB, &tm.z[part], g, n, bar);
-              }
-            }
-          }
-        }
-        if (stop) {
-          // (as the other producer: copies may be landing)
-          *abort_flag = 1;
-          for (int q = max(0, j - C::SLOTS); q < j; ++q)
-            mbar_wait_n(cfull0 + 8 * (q % C::SLOTS), (q / C::SLOTS) & 1, 1u << 12);
-          for (int q = max(0, win - 2); q < win; ++q) mbar_wait_n(wfull0 + 8 * (q & 1), (q >> 1) & 1, 1u << 12);
-        }
-      }
-    } else {
-      // ---------------- dequantize ----------------
-      // the sets of warps that fill a stage (PAIR: 128 rows of B, 4 warps;
-      // single: 256, 8 warps) take turns
-      constexpr int WPS = PAIR ? 4 : 8, SETS = kDeqWarps / WPS;
-      const int dw = warp - 3 - C::EPI, set = dw / WPS;
-      const uint32_t lfull0 = PAIR ? map_rank(full0, 0) : full0;
-      // this thread's 128 bytes of the operand tile: FWD, row r of B; DX, row
-      // r of the step's 64 in block blk of 64 columns.  16-byte pieces are
-      // swizzled by the row, so eight lanes write eight bank groups.
-      const int r = OP == FWD ? (dw % WPS) * 32 + lane : (dw & 1) * 32 + lane;
-      const int blk = OP == FWD ? 0 : (dw % WPS) >> 1;
-      const uint32_t at = C::A_BYTES + (uint32_t)(blk * 8192 + r * 128);
-      const int swz = r & 7;
-      // its codes in a slot, its scales in a window or slot
-      const int crow = OP == FWD ? r & 127 : r, cbox = OP == FWD ? r >> 7 : blk >> 1;
-      const uint32_t codes = stage0 + C::CODE0 + (uint32_t)(cbox * C::BOX + crow * C::ROW);
-      const int cswz = C::swz(crow);
-      const uint32_t sbs = OP == FWD ? stage0 + C::WIN0 + (uint32_t)(2 * cbox * C::SB + crow * 16)
-                                     : stage0 + C::CODE0 + (uint32_t)(C::BOXES * C::BOX + crow * 16);
-      const int nwin = ((s_hi - 1) >> spw) - (s_lo >> spw) + 1;  // windows of a tile
-      const int total = my_tiles * nk;
-      const int64_t G = p.K >> p.lgs;
-      int li = set, lt = 0, n0 = 0;
-      auto settle = [&]() {  // li to a step of tile lt
-        while (li >= nk) li -= nk, ++lt;
-        n0 = lt < my_tiles ? tile_of<OP, PAIR>(p, cluster + lt * clusters).n0 : 0;
-      };
-      // first column of the unit's 64 codes and its two halves' groups
-      auto column = [&]() {
-        return OP == FWD ? (s_lo + li) * kBK : n0 + (PAIR ? 128 * (int)rank : 0) + blk * 64;
-      };
-      // scales and biases of the unit at the cursor, from global memory
-      auto fetch = [&](uint16_t (&sv)[2], uint16_t (&zv)[2]) {
-        const int i = s_lo + li, k = column();
-        int row, part;
-        if constexpr (OP == FWD) {
-          part = PAIR ? (int)rank : r >> 7;
-          row = n0 + (r & 127);
-        } else {
-          part = i >= half;
-          row = (part ? i - half : i) * kBK + r;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kh = k + 32 * h;
-          sv[h] = zv[h] = 0;
-          if (lt < my_tiles && row < p.N && kh < p.K) {  // past the weight: zeros
-            const int64_t g = row * G + (kh >> p.lgs);
-            sv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].scales) + g);
-            zv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].biases) + g);
-          }
-        }
-      };
-      uint16_t sn[2] = {0, 0}, zn[2] = {0, 0};
-      if (total > 0) settle();
-      if (!p.sb_tma && total > 0) fetch(sn, zn);
-      int s = set % S, u = set / S, c = set % C::SLOTS, cu = set / C::SLOTS;
-      for (int j = set; j < total; j += SETS) {
-        const int i = s_lo + li, k = column();
-        uint32_t w[2][B];
-        uint16_t sv[2], zv[2];
-        if (!mbar_wait_abortable(cfull0 + 8 * c, cu & 1, kSpins, abort_flag)) *abort_flag = 1;
-        read_codes<B>(codes + (uint32_t)(c * C::SLOT), OP == FWD ? (B == 3 ? (i & 1) * 24 : 0) : (blk & 1) * 8 * B, cswz,
-                      w);
-        if (p.sb_tma) {
-          uint32_t a = sbs;
-          if constexpr (OP == FWD) {
-            const int win = lt * nwin + (i >> spw) - (s_lo >> spw);
-            if (!mbar_wait_abortable(wfull0 + 8 * (win & 1), (win >> 1) & 1, kSpins, abort_flag)) *abort_flag = 1;
-            a += (uint32_t)((win & 1) * C::WINDOW);
-          } else {
-            a += (uint32_t)(c * C::SLOT);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t o = a + (((k + 32 * h) >> p.lgs) & 7) * 2;
-            sv[h] = lds_u16(o);
-            zv[h] = lds_u16(o + C::SB);
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) sv[h] = sn[h], zv[h] = zn[h];
-        }
-        li += SETS;
-        if (li >= nk) settle();
-        if (!p.sb_tma) fetch(sn, zn);
-        if (u > 0 && !mbar_wait_abortable(empty0 + 8 * s, (u - 1) & 1, kSpins, abort_flag)) *abort_flag = 1;
-        const uint32_t dst = stage0 + (uint32_t)(s * C::STAGE) + at;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          sts_v4(dst + (uint32_t)((q ^ swz) << 4), dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3));
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (PAIR)
-            arrive_remote(lfull0 + 8 * s);
-          else
-            mbar_arrive(full0 + 8 * s);
-          mbar_arrive(cempty0 + 8 * c);
-        }
-        s += SETS;
-        if (s >= S) s -= S, ++u;
-        c += SETS;
-        if (c >= C::SLOTS) c -= C::SLOTS, ++cu;
-      }
-    }
   }
 
   __syncwarp();
   fence_before();
-  if constexpr (!PAIR) {
+  if constexpr (OP != DP) {
     if (splits > 1) {
-      // join the partial tiles: this CTA takes its share of the columns of all
-      // rows, adding the CTAs' partials in rank order
+      // join the partial tiles: this CTA takes its share of the columns of its
+      // 128 rows, adding the partials of the CTAs with the same rows in rank order
       cluster_sync();
       constexpr int COLS = OP == FWD ? 128 : 256;
       const Tile tl = tile_of<OP, PAIR>(p, cluster);
       const int per = COLS / 8 / splits;  // 8-column pieces of this CTA (splits divides 16)
       const bool vec = OP == DX || p.N % 8 == 0;
-      const int rows = min(128, p.M - tl.m0);
+      const int m0 = tl.m0 + 128 * side, rows = min(128, p.M - m0);
       for (int it = threadIdx.x; it < per * 128; it += C::THREADS) {
-        const int row = it & 127, c = ((int)rank * per + (it >> 7)) * 8;
+        const int row = it & 127, c = (split * per + (it >> 7)) * 8;
         if (row >= rows || tl.n0 + c >= (OP == FWD ? p.N : p.K)) continue;
         float v[2][8];
 #pragma unroll
@@ -909,16 +955,17 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[q][i] = 0.0f;
           for (int src = 0; src < splits; ++src) {
-            const uint32_t a = map_rank(stage0 + (uint32_t)(((q * 128 + c) >> 2) * 2048 + row * 16), src);
+            const uint32_t a = map_rank(stage0 + (uint32_t)(((q * 128 + c) >> 2) * 2048 + row * 16),
+                                        PAIR ? 2 * src + side : src);
             const float4 x = lds_cluster(a), y = lds_cluster(a + 2048);
             v[q][0] += x.x; v[q][1] += x.y; v[q][2] += x.z; v[q][3] += x.w;
             v[q][4] += y.x; v[q][5] += y.y; v[q][6] += y.z; v[q][7] += y.w;
           }
         }
         if constexpr (OP == FWD)
-          store_h8<T>(p, tl.m0 + row, tl.n0 + c, v[0], v[1], vec);
+          store_h8<T>(p, m0 + row, tl.n0 + c, v[0], v[1], vec);
         else
-          store8(reinterpret_cast<T*>(p.out[0]) + (int64_t)(tl.m0 + row) * p.K + tl.n0 + c, v[0], true, 8);
+          store8(reinterpret_cast<T*>(p.out[0]) + (int64_t)(m0 + row) * p.K + tl.n0 + c, v[0], true, 8);
       }
     }
   }
@@ -996,7 +1043,7 @@ cudaError_t launch(const Args& p, const Maps& tm, int clusters, cudaStream_t st)
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
-  const int per = PAIR ? 2 : p.splits;
+  const int per = (PAIR ? 2 : 1) * p.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * per);
   cfg.blockDim = dim3(C::THREADS);
