@@ -32,7 +32,8 @@
 // both times).
 //
 // Warps: 0 TMA producer of the activations; 1 TMEM owner and MMA issuer (PAIR:
-// of the leader CTA); 2.. epilogue (4 warps, DP 8); then the producer of the
+// of the leader CTA); 2.. epilogue (4 warps; DP two sets of 8, one for
+// each accumulator); then the producer of the
 // codes and the 16 dequant warps.
 // Every wait is bounded; after one that gave up the tiles are written as NaN.
 #pragma once
@@ -63,7 +64,7 @@ constexpr int kDeqWarps = 16;
 template <int OP, int B, bool PAIR>
 struct Cfg {
   static constexpr bool DENSE = OP == DP || B == 0;                // both operands come by TMA
-  static constexpr int EPI = OP == DP ? 8 : 4;                     // epilogue warps
+  static constexpr int EPI = OP == DP ? 16 : 4;                    // epilogue warps
   static constexpr int DEQ = DENSE ? 0 : kDeqWarps;
   static constexpr int THREADS = (2 + EPI + (DENSE ? 0 : 1) + DEQ) * 32;
   static constexpr int A_BYTES = kTile;                            // 128 rows of A per CTA
@@ -84,7 +85,8 @@ struct Cfg {
   static constexpr int SB = BOX_ROWS * 16;                         // one array, one box
   static constexpr int SLOT = DENSE ? 1024 : (BOXES * BOX + (OP == DX ? 2 * SB : 0) + 1023) / 1024 * 1024;
   static constexpr int WINDOW = OP == FWD ? 2 * BOXES * SB : 0;
-  static constexpr int CODE0 = STAGES * STAGE;
+  static constexpr int OUT0 = STAGES * STAGE;                      // 4 KB a warp to turn rows for storing
+  static constexpr int CODE0 = OUT0 + (OP == DP ? 0 : EPI * 4096);
   static constexpr int AVAIL = 227 * 1024 - 2048 - CODE0 - 2 * WINDOW;
   static constexpr int SLOTS = DENSE ? 0 : AVAIL / SLOT < 8 ? AVAIL / SLOT : 8;
   static constexpr int WIN0 = CODE0 + SLOTS * SLOT;
@@ -95,7 +97,7 @@ struct Cfg {
   static_assert(DENSE || SLOTS >= 3, "room for the codes");
   static_assert(8 * BARS + 8 <= 512, "barriers, TMEM slot and abort flag");
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(128 * 256 * 4 <= CODE0, "a partial tile fits the stages");
+  static_assert(128 * 256 * 4 <= OUT0, "a partial tile fits the stages");
   __device__ static constexpr int swz(int r) {
     return SWZ == 32 ? (r >> 2) & 1 : SWZ == 64 ? (r >> 1) & 3 : SWZ == 128 ? r & 7 : 0;
   }
@@ -338,6 +340,36 @@ __device__ __forceinline__ uint4 dequant8(const uint32_t (&w)[B], uint16_t scale
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2f(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+// 2^23 + code i of 32
+template <int B>
+__device__ __forceinline__ float code_2p23(const uint32_t (&w)[B], int i) {
+  if constexpr (B == 8) {
+    return __uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440u | (uint32_t)(i & 3)));
+  } else if constexpr (B == 4) {
+    const uint32_t t = (i & 1) ? (w[i >> 3] >> 4) & 0x0F0F0F0Fu : w[i >> 3] & 0x0F0F0F0Fu;
+    return __uint_as_float(__byte_perm(t, 0x4B000000u, 0x7440u | (uint32_t)((i >> 1) & 3)));
+  } else {
+    return __uint_as_float(0x4B000000u | stream_code<B>(w, i));
+  }
+}
+
 // 32 codes of a row in global memory
 template <int B>
 __device__ __forceinline__ void load_words(const uint32_t* src, uint32_t (&w)[B]) {
@@ -429,6 +461,66 @@ __device__ __forceinline__ void store8(T* dst, const float* v, bool vec, int cnt
   }
 }
 
+// SiLU(g) * u within 2^-19
+__device__ __forceinline__ float silu_mul(float g, float u) { return g * __fdividef(1.0f, 1.0f + __expf(-g)) * u; }
+
+// A warp's 32 rows of 128 bytes, row `lane` written by that lane in 16-byte
+// pieces swizzled by the row, then stored so that a row's 128 bytes leave
+// together: 4 rows an instruction, where a lane's own row would touch 32 lines.
+template <typename T>
+struct Turn {
+  static constexpr int COLS = 128 / (int)sizeof(T);
+  uint32_t buf;
+  int lane;
+  // columns c .. c + 7 of the lane's row
+  __device__ __forceinline__ void put8(int c, const float* v) const {
+    const uint32_t row = buf + (uint32_t)(lane * 128);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        sts_v4(row + (uint32_t)((((c >> 2) + h) ^ (lane & 7)) << 4),
+               make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                          __float_as_uint(v[4 * h + 3])));
+    } else {
+      sts_v4(row + (uint32_t)(((c >> 3) ^ (lane & 7)) << 4),
+             make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])));
+    }
+  }
+  // to dst (row 0, column 0 of the piece), rows of ld elements; vec: 16-byte rows
+  __device__ __forceinline__ void flush(T* dst, int64_t ld, int rows, int cols, bool vec) const {
+    __syncwarp();
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = i * 4 + (lane >> 3), c = lane & 7;
+        const uint4 v = lds_v4(buf + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)));
+        if (row < rows && c * (16 / (int)sizeof(T)) < cols)
+          *reinterpret_cast<uint4*>(dst + row * ld + c * (16 / (int)sizeof(T))) = v;
+      }
+    } else {
+#pragma unroll 8
+      for (int row = 0; row < 32; ++row) {
+#pragma unroll
+        for (int c = lane; c < COLS; c += 32) {
+          const int byte = c * (int)sizeof(T);
+          const uint32_t a = buf + (uint32_t)(row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
+          if (c < cols && row < rows) {
+            if constexpr (sizeof(T) == 4) {
+              float v;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+              dst[row * ld + c] = v;
+            } else {
+              const uint16_t v = lds_u16(a);
+              memcpy(dst + row * ld + c, &v, 2);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+};
+
 // h (and g, u) of 8 columns from column n of row m
 template <typename T>
 __device__ __forceinline__ void store_h8(const Args& p, int m, int n, const float* g, const float* u, bool vec) {
@@ -437,7 +529,7 @@ __device__ __forceinline__ void store_h8(const Args& p, int m, int n, const floa
   const int64_t at = (int64_t)m * p.N + n;
   float h[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = g[i] * __fdividef(1.0f, 1.0f + __expf(-g[i])) * u[i];  // within 2^-19
+  for (int i = 0; i < 8; ++i) h[i] = silu_mul(g[i], u[i]);
   if (p.out_dtype == QMM_F32)
     store8(reinterpret_cast<float*>(p.out[0]) + at, h, vec, cnt);
   else
@@ -491,7 +583,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf0 + 8 * b, 1);
-      mbar_init(tfree0 + 8 * b, C::EPI * (PAIR ? 2 : 1));
+      mbar_init(tfree0 + 8 * b, (OP == DP ? 8 : C::EPI) * (PAIR ? 2 : 1));
     }
     mbar_init(drain, 1);
     for (int s = 0; s < C::SLOTS; ++s) {
@@ -812,9 +904,22 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
     const uint32_t ltfree0 = PAIR ? map_rank(tfree0, lead) : tfree0;
     const float nan = __int_as_float(0x7fc00000);
     bool failed = false;
-    for (int lt = 0; lt < my_tiles; ++lt) {
+    // (DP: two sets of 8 warps, one for each accumulator)
+    for (int lt = OP == DP ? (warp - 2) >> 3 : 0; lt < my_tiles; lt += OP == DP ? 2 : 1) {
       const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
       const int b = lt & 1;
+      const int row = tl.m0 + 128 * side + r;
+      // DP: the codes of the lane's row, requested while the products run
+      uint32_t codes[4][B ? B : 1];
+      const int c0 = OP == DP ? (((warp - 2) >> 2) & 1) * 128 : 0;
+      if constexpr (OP == DP) {
+#pragma unroll
+        for (int un = 0; un < 4; ++un) {
+          const int k = tl.n0 + c0 + un * 32;
+          if (row < p.N && k < p.K)
+            load_words<B>(p.w[tl.part].packed + ((int64_t)row * (p.K >> 5) + (k >> 5)) * B, codes[un]);
+        }
+      }
       if (!failed) {
         failed = !wait(accf0 + 8 * b, (lt >> 1) & 1, abort_flag) ||
                  *reinterpret_cast<volatile int*>(abort_flag);
@@ -822,21 +927,17 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
       }
       fence_after();
       const uint32_t acc = lanes + (uint32_t)(b * 256);
-      const int row = tl.m0 + 128 * side + r;
       if constexpr (OP == DP) {
         // 128 columns of one weight row: units of 32, groups of 1, 2 or 4
-        const int c0 = ((warp - 2) >> 2) * 128;
         const int lu = p.lgs - 5;  // log2 of the units per group
         const int64_t G = p.K >> p.lgs;
         const bool live = row < p.N;
-        float ds = 0.0f, dz = 0.0f;
+        float2 sq = make_float2(0.0f, 0.0f), sv = sq;
 #pragma unroll
         for (int un = 0; un < 4; ++un) {
           const int k = tl.n0 + c0 + un * 32;
           if (k < p.K) {
-            uint32_t w[B];
-            if (live) load_words<B>(p.w[tl.part].packed + ((int64_t)row * (p.K >> 5) + (k >> 5)) * B, w);
-            float sq = 0.0f, sv = 0.0f;
+            const uint32_t(&w)[B] = codes[un];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               float v[16];
@@ -849,23 +950,23 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
               }
               if (live) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  // q / 2^B: the code in the top mantissa bits of 1.0, less 1.0
-                  const uint32_t q = stream_code<B>(w, hf * 16 + i);
-                  sq = fmaf(v[i], __uint_as_float(0x3F800000u | (q << (23 - B))) - 1.0f, sq);
-                  sv += v[i];
+                for (int i = 0; i < 16; i += 2) {
+                  const float2 x = make_float2(v[i], v[i + 1]);
+                  // 2^23 + q, less 2^23: exact
+                  const float2 q = add2(make_float2(code_2p23<B>(w, hf * 16 + i), code_2p23<B>(w, hf * 16 + i + 1)),
+                                        make_float2(-8388608.0f, -8388608.0f));
+                  sq = fma2f(x, q, sq);
+                  sv = add2(sv, x);
                 }
               }
             }
-            ds += sq * (float)(1 << B);
-            dz += sv;
             if (((un + 1) & ((1 << lu) - 1)) == 0) {
               if (live) {
                 const int64_t at = (int64_t)row * G + (k >> p.lgs);
-                store_as(p.out[2 * tl.part], p.out_dtype, at, ds);
-                store_as(p.out[2 * tl.part + 1], p.out_dtype, at, dz);
+                store_as(p.out[2 * tl.part], p.out_dtype, at, sq.x + sq.y);
+                store_as(p.out[2 * tl.part + 1], p.out_dtype, at, sv.x + sv.y);
               }
-              ds = dz = 0.0f;
+              sq = sv = make_float2(0.0f, 0.0f);
             }
           }
         }
@@ -889,9 +990,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
         }
       } else if constexpr (OP == FWD) {
         const bool vec = p.N % 8 == 0;
-#pragma unroll 1
-        for (int c = first; c < 128 && tl.n0 + c < p.N; c += stride) {
-          float g[16], u[16];
+        auto read = [&](int c, float (&g)[16], float (&u)[16]) {
           if (!failed) {
             tmem_ld16(acc + (uint32_t)c, g);
             tmem_ld16(acc + (uint32_t)(128 + c), u);
@@ -900,15 +999,61 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
 #pragma unroll
             for (int i = 0; i < 16; ++i) g[i] = u[i] = nan;
           }
-          if (row < p.M) {
-            store_h8<T>(p, row, tl.n0 + c, g, u, vec);
-            store_h8<T>(p, row, tl.n0 + c + 8, g + 8, u + 8, vec);
+        };
+        if (only && vec) {  // each lane stores its own row: more warps at work
+#pragma unroll 1
+          for (int c = first; c < 128 && tl.n0 + c < p.N; c += stride) {
+            float g[16], u[16];
+            read(c, g, u);
+            if (row < p.M) {
+              store_h8<T>(p, row, tl.n0 + c, g, u, vec);
+              store_h8<T>(p, row, tl.n0 + c + 8, g + 8, u + 8, vec);
+            }
+          }
+        } else {
+          // what 0: h, 1: g, 2: u, each 128 bytes of 32 rows at a time, dealt to
+          // the warps of the lane quarter (all done reading the stages, if several)
+          const uint32_t buf = stage0 + (uint32_t)((only ? 0 : C::OUT0) + (warp - 2) * 4096);
+          int job = -(first >> 4);
+          auto piece = [&](auto type, int what) {
+            using O = decltype(type);
+            const Turn<O> out{buf, lane};
+            const int row0 = row - lane;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 128 && tl.n0 + c0 < p.N; c0 += Turn<O>::COLS) {
+              if (job++ % (stride >> 4) != 0) continue;
+#pragma unroll 1
+              for (int c = 0; c < Turn<O>::COLS; c += 16) {
+                float g[16], u[16];
+                if (what == 0) {
+                  read(c0 + c, g, u);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) g[i] = silu_mul(g[i], u[i]);
+                } else if (!failed) {
+                  tmem_ld16(acc + (uint32_t)((what - 1) * 128 + c0 + c), g);
+                  tmem_wait();
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) g[i] = nan;
+                }
+                out.put8(c, g);
+                out.put8(c + 8, g + 8);
+              }
+              out.flush(reinterpret_cast<O*>(p.out[what]) + (int64_t)row0 * p.N + tl.n0 + c0, p.N, p.M - row0,
+                        p.N - tl.n0 - c0, vec);
+            }
+          };
+          if (p.out_dtype == QMM_F32)
+            piece(float(), 0);
+          else
+            piece(T(), 0);
+          if (p.out[1]) {
+            piece(T(), 1);
+            piece(T(), 2);
           }
         }
       } else {
-#pragma unroll 1
-        for (int c = first; c < 256 && tl.n0 + c < p.K; c += stride) {
-          float v[16];
+        auto read = [&](int c, float (&v)[16]) {
           if (!failed) {
             tmem_ld16(acc + (uint32_t)c, v);
             tmem_wait();
@@ -916,10 +1061,32 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = nan;
           }
-          if (row < p.M) {
-            T* dst = reinterpret_cast<T*>(p.out[0]) + (int64_t)row * p.K + tl.n0 + c;
-            store8(dst, v, true, 8);
-            store8(dst + 8, v + 8, true, 8);
+        };
+        if (only) {
+#pragma unroll 1
+          for (int c = first; c < 256 && tl.n0 + c < p.K; c += stride) {
+            float v[16];
+            read(c, v);
+            if (row < p.M) {
+              T* dst = reinterpret_cast<T*>(p.out[0]) + (int64_t)row * p.K + tl.n0 + c;
+              store8(dst, v, true, 8);
+              store8(dst + 8, v + 8, true, 8);
+            }
+          }
+        } else {
+          const Turn<T> out{stage0 + (uint32_t)(C::OUT0 + (warp - 2) * 4096), lane};
+          const int row0 = row - lane;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256 && tl.n0 + c0 < p.K; c0 += Turn<T>::COLS) {
+#pragma unroll 1
+            for (int c = 0; c < Turn<T>::COLS; c += 16) {
+              float v[16];
+              read(c0 + c, v);
+              out.put8(c, v);
+              out.put8(c + 8, v + 8);
+            }
+            out.flush(reinterpret_cast<T*>(p.out[0]) + (int64_t)row0 * p.K + tl.n0 + c0, p.K, p.M - row0,
+                      p.K - tl.n0 - c0, true);
           }
         }
       }
