@@ -425,7 +425,7 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
  * QMM_ERR_BAD_TOKEN_ID in *d_status (may be NULL).  n == 0 is a no-op.
  * Errors: qmm_dequantize's for w; DTYPE (out_dtype), INVALID_ARG (n outside
  * [0, 2^31 - 1]), ALIGNMENT (ids and d_status 4-byte, out 16-byte),
- * UNSUPPORTED (device), CUDA. */
+ * UNSUPPORTED (more than 2^25 columns, device), CUDA. */
 qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha, void* out,
                          qmm_dtype out_dtype, int32_t* d_status, void* stream);
 

@@ -9,53 +9,130 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "mx.cuh"
 
 namespace qmm {
 namespace embed {
 
-// One thread per 32 codes of one token's row (B words, whole groups of 16 or
-// part of one larger group).
+template <typename K, typename A>
+static cudaError_t launch_next(K kernel, dim3 grid, int threads, size_t smem, int cluster, const A& args, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+// 8 codes (B bytes, 1- or 2-byte aligned for 3- and 6-bit codes) as words
+template <int B>
+__device__ __forceinline__ void load8(const uint8_t* src, uint32_t (&w)[3]) {
+  w[0] = w[1] = w[2] = 0u;
+  if constexpr (B == 8) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
+    w[0] = q.x;
+    w[1] = q.y;
+  } else if constexpr (B == 4) {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  } else if constexpr (B == 2 || B == 6) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+    w[0] = __ldg(h);
+    if constexpr (B == 6) {
+      w[0] |= (uint32_t)__ldg(h + 1) << 16;
+      w[1] = __ldg(h + 2);
+    }
+  } else {
+    w[0] = __ldg(src) | ((uint32_t)__ldg(src + 1) << 8) | ((uint32_t)__ldg(src + 2) << 16);
+  }
+}
+
+constexpr int kLookThreads = 256;
+constexpr int kLookTokens = 4;  // rows a thread has in flight
+
+struct LookArgs {
+  const int32_t* ids;
+  const uint32_t* packed;
+  const void* scales;
+  const void* biases;
+  int rows, n;
+  int pieces, lgs;      // pieces: 8 columns each
+  int lanes;            // threads of a block on one row: a power of two
+  float alpha;
+  void* out;
+  int32_t* d_status;
+};
+
+// A thread turns 8 codes of a row into 8 outputs, so that a warp's stores are
+// contiguous.  The bound is the output's bytes; what hides the two dependent
+// loads (the id, then the row) is kLookTokens rows in flight per thread
+// (16384 rows of 4096 columns: 45 us with 32 codes of one row a thread).
 template <int B, int MODE, typename TS, typename TO>
-__global__ void __launch_bounds__(256)
-lookup_kernel(const int32_t* __restrict__ ids, int64_t n, const uint32_t* __restrict__ packed,
-              const void* __restrict__ scales, const void* __restrict__ biases, int64_t rows, int64_t cols, int gs,
-              float alpha, TO* __restrict__ out, int32_t* d_status) {
-  const int64_t chunks = cols / 32, G = cols / gs;
-  for (int64_t idx = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; idx < n * chunks;
-       idx += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = idx / chunks, c = idx - t * chunks;
-    const int64_t r = __ldg(ids + t);
-    __align__(16) TO vals[32];
-    if (r < 0 || r >= rows) {
-      if (c == 0) set_status(d_status, QMM_ERR_BAD_TOKEN_ID);
+__global__ void __launch_bounds__(kLookThreads) lookup_kernel(const LookArgs p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per_block = kLookThreads / p.lanes;  // rows of a block at a time
+  const int c = blockIdx.y * p.lanes + threadIdx.x % p.lanes;
+  const int step = gridDim.x * per_block;
+  if (c >= p.pieces) return;
+  const int per_group = p.lgs - 3, G = p.pieces >> per_group, g0 = c >> per_group;
+  const float2 alpha = make_float2(p.alpha, p.alpha);
+  for (int64_t t0 = blockIdx.x * per_block + threadIdx.x / p.lanes; t0 < p.n; t0 += kLookTokens * step) {
+    int row[kLookTokens];
+    uint32_t w[kLookTokens][3];
+    float s[kLookTokens], b[kLookTokens];
+    bool ok[kLookTokens];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) vals[i] = from_f32<TO>(0.0f);
-    } else {
-      const uint32_t* src = packed + r * (cols * B / 32) + c * B;
-      uint32_t wr[B + 1];
+    for (int u = 0; u < kLookTokens; ++u) row[u] = t0 + u * step < p.n ? __ldg(p.ids + t0 + u * step) : 0;
 #pragma unroll
-      for (int i = 0; i < B; ++i) wr[i] = __ldg(src + i);
-      wr[B] = 0u;
-      if constexpr (MODE == QMM_MODE_AFFINE) {
-        const float s = to_f32(reinterpret_cast<const TS*>(scales)[r * G + c * 32 / gs]);
-        const float b = to_f32(reinterpret_cast<const TS*>(biases)[r * G + c * 32 / gs]);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          vals[i] = from_f32<TO>(__fmul_rn(alpha, fmaf((float)stream_code<B>(wr, i), s, b)));
-      } else {
-        using Md = mx::Mode<MODE>;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float s = Md::scale(__ldg(reinterpret_cast<const uint8_t*>(scales) + r * G + (c * 32 + i) / Md::GS));
-          vals[i] = from_f32<TO>(__fmul_rn(alpha, Md::lane(stream_code<B>(wr, i)) * s));
+    for (int u = 0; u < kLookTokens; ++u) {
+      ok[u] = (uint32_t)row[u] < (uint32_t)p.rows;
+      if (ok[u] && t0 + u * step < p.n) {
+        load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)row[u] * p.pieces + c) * B, w[u]);
+        const int64_t g = (int64_t)row[u] * G + g0;
+        if constexpr (MODE == QMM_MODE_AFFINE) {
+          s[u] = to_f32(__ldg(reinterpret_cast<const TS*>(p.scales) + g));
+          b[u] = to_f32(__ldg(reinterpret_cast<const TS*>(p.biases) + g));
+        } else {
+          s[u] = mx::Mode<MODE>::scale(__ldg(reinterpret_cast<const uint8_t*>(p.scales) + g));
         }
       }
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + t * cols + c * 32);
-    const uint4* v4 = reinterpret_cast<const uint4*>(vals);
 #pragma unroll
-    for (int i = 0; i < (int)(32 * sizeof(TO) / 16); ++i) dst[i] = v4[i];
+    for (int u = 0; u < kLookTokens; ++u) {
+      if (t0 + u * step >= p.n) break;
+      __align__(16) TO v[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        float2 x;
+        if constexpr (MODE == QMM_MODE_AFFINE)
+          x = mul2(alpha, fma2f(codes2<B>(w[u], i), make_float2(s[u], s[u]), make_float2(b[u], b[u])));
+        else
+          x = mul2(alpha, mul2(make_float2(mx::Mode<MODE>::lane(stream_code<B>(w[u], i)),
+                                           mx::Mode<MODE>::lane(stream_code<B>(w[u], i + 1))),
+                               make_float2(s[u], s[u])));
+        v[i] = from_f32<TO>(x.x);
+        v[i + 1] = from_f32<TO>(x.y);
+      }
+      uint4 o[sizeof(TO) / 2];
+      memcpy(o, v, sizeof(o));
+      if (!ok[u]) {
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(TO) / 2; ++h) o[h] = make_uint4(0u, 0u, 0u, 0u);
+        if (c == 0) set_status(p.d_status, QMM_ERR_BAD_TOKEN_ID);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<TO*>(p.out) + ((t0 + u * step) * p.pieces + c) * 8);
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(TO) / 2; ++h) dst[h] = o[h];
+    }
   }
 }
 
@@ -69,6 +146,7 @@ lookup_kernel(const int32_t* __restrict__ ids, int64_t n, const uint32_t* __rest
 // once: the bound is dy's bytes (and the output's, zeros included).
 constexpr int kSortThreads = 1024, kSortWarps = 32;
 constexpr int kSortCtas = 8;        // one cluster sorts
+constexpr int kHeld = 2;            // list entries a lane keeps between a pass's two readings
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSlabThreads = 128;   // 8 columns each
 constexpr int kSlab = kSlabThreads * 8;
@@ -138,8 +216,16 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs p)
     };
     for (int i = tid; i < kSortWarps * kDigits; i += kSortThreads) hist[i] = 0u;
     __syncthreads();
-    for (int i = lo + lane; i < hi; i += 32) {
-      const uint32_t k = key_at(i);
+    // (the first kHeld rounds' entries stay in registers for the scatter)
+    uint32_t hk[kHeld], hp[kHeld];
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      const int i = lo + 32 * r + lane;
+      hk[r] = i < hi ? key_at(i) : 0u;
+      hp[r] = i < hi ? (pass ? src_p[i] : (uint32_t)i) : 0u;
+    }
+    for (int i = lo + lane, r = 0; i < hi; i += 32, ++r) {
+      const uint32_t k = r == 0 ? hk[0] : r == 1 ? hk[1] : key_at(i);
       if (pass == 0 && k == (uint32_t)p.rows) set_status(p.d_status, QMM_ERR_BAD_TOKEN_ID);
       atomicAdd(mine + ((k >> shift) & mask), 1u);
     }
@@ -178,12 +264,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs p)
       base[tid] = off + incl - all + before;
     }
     __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32) {
+    for (int i0 = lo, rr = 0; i0 < hi; i0 += 32, ++rr) {
       const int i = i0 + lane;
       const bool in = i < hi;
       const uint32_t act = __ballot_sync(0xffffffffu, in);
       if (in) {
-        const uint32_t k = key_at(i), t = pass ? src_p[i] : (uint32_t)i;
+        const uint32_t k = rr == 0 ? hk[0] : rr == 1 ? hk[1] : key_at(i);
+        const uint32_t t = rr == 0 ? hp[0] : rr == 1 ? hp[1] : pass ? src_p[i] : (uint32_t)i;
         const uint32_t d = (k >> shift) & mask;
         const uint32_t peers = __match_any_sync(act, d);
         const int r = __popc(peers & ((1u << lane) - 1u));
@@ -229,21 +316,27 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
   const int64_t G = p.cols >> p.lgs;
   const int lpg = 1 << (p.lgs - 3);  // threads of a group
   constexpr int U = sizeof(TD) == 4 ? 4 : 8;  // rows requested at a time
+  const uint32_t after = __shfl_down_sync(0xffffffffu, key, 1);
+  // the entries after which a run or the chunk ends
+  const uint32_t ends = __ballot_sync(0xffffffffu, lane < cnt && (lane + 1 == cnt || after != key));
   float acc[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
   int start = 0;
   for (int i0 = 0; i0 < cnt; i0 += U) {
+    // U rows of dy, and the codes of the rows whose runs end among them
     uint4 raw[U][sizeof(TD) / 2];
+    uint32_t code[U][3];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const uint32_t t = __shfl_sync(0xffffffffu, tok, (i0 + j) & 31);
       const uint32_t k = __shfl_sync(0xffffffffu, key, (i0 + j) & 31);
+      const bool in = i0 + j < cnt && live && k < (uint32_t)p.rows;
 #pragma unroll
       for (int h = 0; h < (int)sizeof(TD) / 2; ++h)
-        raw[j][h] = i0 + j < cnt && live && k < (uint32_t)p.rows
-                        ? __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)t * p.cols) + h)
-                        : make_uint4(0u, 0u, 0u, 0u);
+        raw[j][h] = in ? __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)t * p.cols) + h) : make_uint4(0u, 0u, 0u, 0u);
+      if (in && (ends >> (i0 + j) & 1u))
+        load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)k * p.cols + col) / 8 * B, code[j]);
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
@@ -253,34 +346,14 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
       memcpy(v, raw[j], sizeof(v));
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] += to_f32(v[c]);
+      if (!(ends >> i & 1u)) continue;  // the run goes on
       const uint32_t k = __shfl_sync(0xffffffffu, key, i);
-      const uint32_t kn = i + 1 < cnt ? __shfl_sync(0xffffffffu, key, i + 1) : next;
-      if (k == kn && i + 1 < cnt) continue;  // the run goes on
       if (k < (uint32_t)p.rows) {
-        // the run ends here, or the chunk does
         float ds = 0.0f, db = 0.0f;
         if (live) {
-          uint32_t w[3] = {0u, 0u, 0u};
-          const uint8_t* src = reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)k * p.cols + col) / 8 * B;
-          if constexpr (B == 8) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
-            w[0] = q.x;
-            w[1] = q.y;
-          } else if constexpr (B == 4) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-          } else if constexpr (B == 2 || B == 6) {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
-            w[0] = __ldg(h);
-            if constexpr (B == 6) {
-              w[0] |= (uint32_t)__ldg(h + 1) << 16;
-              w[1] = __ldg(h + 2);
-            }
-          } else {
-            w[0] = __ldg(src) | ((uint32_t)__ldg(src + 1) << 8) | ((uint32_t)__ldg(src + 2) << 16);
-          }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            ds = fmaf(acc[c], (float)stream_code<B>(w, c), ds);
+            ds = fmaf(acc[c], code_2p23<B>(code[j], c) - 8388608.0f, ds);
             db += acc[c];
           }
         }
@@ -319,11 +392,20 @@ __global__ void __launch_bounds__(128) join_kernel(const GradArgs p) {
   const bool whole = p.keys[e0] == k;  // it fills this chunk
   if (whole && e0 > 0 && p.keys[e0 - 1] == k) return;  // it began earlier
   const int64_t G = p.cols >> p.lgs;
-  int pieces = 1;  // further chunks of the run
-  while ((int64_t)(chunk + pieces) * p.chunk + p.chunk < p.n && p.keys[(chunk + pieces + 1) * p.chunk] == k) ++pieces;
+  // further chunks that begin with the run, 32 looked at together
+  int pieces = 0;
+  for (;;) {
+    const int64_t at = (int64_t)(chunk + 1 + pieces + (int)(threadIdx.x & 31)) * p.chunk;
+    const uint32_t same = __ballot_sync(0xffffffffu, at < p.n && p.keys[at] == k);
+    if (same != 0xffffffffu) {
+      pieces += __ffs(~same) - 1;
+      break;
+    }
+    pieces += 32;
+  }
   for (int64_t g = threadIdx.x; g < 2 * G; g += blockDim.x) {
     float sum = p.part[((int64_t)chunk * 2 + (whole ? 0 : 1)) * 2 * G + g];
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 1; c <= pieces; ++c) sum += p.part[(int64_t)(chunk + c) * 4 * G + g];
     store_as(p.out[g >= G], p.g_dtype, (int64_t)k * G + (g >= G ? g - G : g), p.alpha * sum);
   }
@@ -343,37 +425,22 @@ static int64_t grad_workspace(int64_t n, int64_t cols) {
   return 16 + (n + 3) / 4 * 16 * 4 + chunks * 4 * ((cols + 31) / 32) * 4;
 }
 
-template <typename K, typename A>
-static cudaError_t launch_next(K kernel, dim3 grid, int threads, size_t smem, int cluster, const A& args, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
-}
-
 template <int B, int MODE, typename TS>
 static cudaError_t lookup_o(const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha, void* out, int out_dtype,
                             int32_t* d_status, cudaStream_t st) {
-  const int64_t items = n * (w->cols / 32);
-  const int grid = (int)std::min<int64_t>((items + 255) / 256, 148 * 64);
-#define QMM_L(TO)                                                                                              \
-  lookup_kernel<B, MODE, TS, TO><<<grid, 256, 0, st>>>(ids, n, w->packed, w->scales, w->biases, w->rows, w->cols, \
-                                                       w->group_size, alpha, (TO*)out, d_status)
-  if (out_dtype == QMM_F32) QMM_L(float);
-  else if (out_dtype == QMM_BF16) QMM_L(__nv_bfloat16);
-  else QMM_L(__half);
-#undef QMM_L
-  return cudaGetLastError();
+  LookArgs a{ids, w->packed, w->scales, w->biases, (int)std::min<int64_t>(w->rows, INT32_MAX), (int)n, (int)(w->cols / 8), 4, kLookThreads, alpha, out,
+             d_status};
+  while ((1 << a.lgs) < w->group_size) ++a.lgs;  // 16 (nvfp4), 32, 64 or 128
+  while (a.lanes / 2 >= a.pieces) a.lanes /= 2;
+  const int per_block = kLookThreads / a.lanes;
+  const int64_t tiles = ((int64_t)a.pieces + a.lanes - 1) / a.lanes;
+  // one row a thread while SMs are idle, then up to kLookTokens
+  const int64_t want = (n + per_block - 1) / per_block;
+  const int64_t most = std::max<int64_t>(1, (int64_t)qmm_host::num_sms() * 16 / tiles);
+  const dim3 grid((unsigned)std::min(want, most), (unsigned)tiles);
+  if (out_dtype == QMM_F32) return launch_next(lookup_kernel<B, MODE, TS, float>, grid, kLookThreads, 0, 1, a, st);
+  if (out_dtype == QMM_BF16) return launch_next(lookup_kernel<B, MODE, TS, __nv_bfloat16>, grid, kLookThreads, 0, 1, a, st);
+  return launch_next(lookup_kernel<B, MODE, TS, __half>, grid, kLookThreads, 0, 1, a, st);
 }
 
 template <int B>
@@ -476,6 +543,7 @@ qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, fl
   if (s != QMM_OK) return s;
   if (!dtype_ok(out_dtype)) return QMM_ERR_DTYPE;
   if (n < 0 || n > (int64_t)INT32_MAX) return QMM_ERR_INVALID_ARG;
+  if (w->cols > (1 << 25)) return QMM_ERR_UNSUPPORTED;
   if (d_status && !aligned4(d_status)) return QMM_ERR_ALIGNMENT;
   if (n == 0) return QMM_OK;
   if (!aligned4(ids) || !aligned16(out)) return QMM_ERR_ALIGNMENT;

@@ -43,6 +43,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "mbarrier.cuh"
 
 namespace qmm {
@@ -338,36 +339,6 @@ __device__ __forceinline__ uint4 dequant8(const uint32_t (&w)[B], uint16_t scale
     for (int e = 0; e < 4; ++e) v[e] = fma2<T>(sub2<T>(p[e], OFF2), s2, z2);
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-// two fp32 operations in one instruction
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2f(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-// 2^23 + code i of 32
-template <int B>
-__device__ __forceinline__ float code_2p23(const uint32_t (&w)[B], int i) {
-  if constexpr (B == 8) {
-    return __uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440u | (uint32_t)(i & 3)));
-  } else if constexpr (B == 4) {
-    const uint32_t t = (i & 1) ? (w[i >> 3] >> 4) & 0x0F0F0F0Fu : w[i >> 3] & 0x0F0F0F0Fu;
-    return __uint_as_float(__byte_perm(t, 0x4B000000u, 0x7440u | (uint32_t)((i >> 1) & 3)));
-  } else {
-    return __uint_as_float(0x4B000000u | stream_code<B>(w, i));
-  }
 }
 
 // 32 codes of a row in global memory
@@ -952,9 +923,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                   const float2 x = make_float2(v[i], v[i + 1]);
-                  // 2^23 + q, less 2^23: exact
-                  const float2 q = add2(make_float2(code_2p23<B>(w, hf * 16 + i), code_2p23<B>(w, hf * 16 + i + 1)),
-                                        make_float2(-8388608.0f, -8388608.0f));
+                  const float2 q = codes2<B>(w, hf * 16 + i);
                   sq = fma2f(x, q, sq);
                   sv = add2(sv, x);
                 }
