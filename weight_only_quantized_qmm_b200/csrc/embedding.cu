@@ -311,17 +311,17 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
   const uint32_t tok = lane < cnt ? p.perm[e0 + lane] : 0u;
   const uint32_t prev = e0 > 0 ? p.keys[e0 - 1] : 0xffffffffu, next = e0 + cnt < p.n ? p.keys[e0 + cnt] : 0xffffffffu;
   const int col = blockIdx.y * kSlab + threadIdx.x * 8;
-  const bool live = col < p.cols;
-  const TD* dy = reinterpret_cast<const TD*>(p.dy) + col;
+  const bool live = col < p.cols;  // (threads past the row read its start and store nothing)
+  const TD* dy = reinterpret_cast<const TD*>(p.dy) + (live ? col : 0);
   const int64_t G = p.cols >> p.lgs;
   const int lpg = 1 << (p.lgs - 3);  // threads of a group
   constexpr int U = sizeof(TD) == 4 ? 4 : 8;  // rows requested at a time
   const uint32_t after = __shfl_down_sync(0xffffffffu, key, 1);
   // the entries after which a run or the chunk ends
   const uint32_t ends = __ballot_sync(0xffffffffu, lane < cnt && (lane + 1 == cnt || after != key));
-  float acc[8];
+  float2 acc[4];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+  for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.0f, 0.0f);
   int start = 0;
   for (int i0 = 0; i0 < cnt; i0 += U) {
     // U rows of dy, and the codes of the rows whose runs end among them
@@ -329,14 +329,16 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
     uint32_t code[U][3];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const uint32_t t = __shfl_sync(0xffffffffu, tok, (i0 + j) & 31);
-      const uint32_t k = __shfl_sync(0xffffffffu, key, (i0 + j) & 31);
-      const bool in = i0 + j < cnt && live && k < (uint32_t)p.rows;
+      // (lanes past the chunk hold token 0: a valid row, and what a bad id's
+      // tokens add is dropped with their run)
+      const int64_t t = __shfl_sync(0xffffffffu, tok, (i0 + j) & 31);
 #pragma unroll
-      for (int h = 0; h < (int)sizeof(TD) / 2; ++h)
-        raw[j][h] = in ? __ldcs(reinterpret_cast<const uint4*>(dy + (int64_t)t * p.cols) + h) : make_uint4(0u, 0u, 0u, 0u);
-      if (in && (ends >> (i0 + j) & 1u))
-        load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)k * p.cols + col) / 8 * B, code[j]);
+      for (int h = 0; h < (int)sizeof(TD) / 2; ++h) raw[j][h] = __ldcs(reinterpret_cast<const uint4*>(dy + t * p.cols) + h);
+      if (ends >> ((i0 + j) & 31) & 1u) {
+        const uint32_t k = __shfl_sync(0xffffffffu, key, (i0 + j) & 31);
+        if (live && k < (uint32_t)p.rows)
+          load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)k * p.cols + col) / 8 * B, code[j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
@@ -345,18 +347,19 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
       __align__(16) TD v[8];
       memcpy(v, raw[j], sizeof(v));
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] += to_f32(v[c]);
+      for (int c = 0; c < 4; ++c) acc[c] = add2(acc[c], make_float2(to_f32(v[2 * c]), to_f32(v[2 * c + 1])));
       if (!(ends >> i & 1u)) continue;  // the run goes on
       const uint32_t k = __shfl_sync(0xffffffffu, key, i);
       if (k < (uint32_t)p.rows) {
-        float ds = 0.0f, db = 0.0f;
+        float2 s2 = make_float2(0.0f, 0.0f), b2 = s2;
         if (live) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            ds = fmaf(acc[c], code_2p23<B>(code[j], c) - 8388608.0f, ds);
-            db += acc[c];
+          for (int c = 0; c < 4; ++c) {
+            s2 = fma2f(acc[c], codes2<B>(code[j], 2 * c), s2);
+            b2 = add2(b2, acc[c]);
           }
         }
+        float ds = s2.x + s2.y, db = b2.x + b2.y;
         for (int o = 1; o < lpg; o <<= 1) {
           ds += __shfl_xor_sync(0xffffffffu, ds, o);
           db += __shfl_xor_sync(0xffffffffu, db, o);
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
         }
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+      for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.0f, 0.0f);
       start = i + 1;
     }
   }
