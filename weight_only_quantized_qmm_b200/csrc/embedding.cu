@@ -144,9 +144,8 @@ __global__ void __launch_bounds__(kLookThreads) lookup_kernel(const LookArgs p) 
 // runs inside a chunk are stored at once, those that cross its ends leave
 // partial group sums that the join adds in list order.  Everything is read
 // once: the bound is dy's bytes (and the output's, zeros included).
-constexpr int kSortThreads = 1024, kSortWarps = 32;
-constexpr int kSortCtas = 8;        // one cluster sorts
-constexpr int kHeld = 2;            // list entries a lane keeps between a pass's two readings
+constexpr int kSortThreads = 512, kSortWarps = 16;  // of each sorting CTA
+constexpr int kHeld = 4;            // list entries a lane keeps between a pass's two readings
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSlabThreads = 128;   // 8 columns each
 constexpr int kSlab = kSlabThreads * 8;
@@ -156,6 +155,7 @@ struct SortArgs {
   int n;
   int rows;
   int passes, bits;      // digits of the keys and bits of a digit
+  int ctas;              // that sort: one, or a cluster of 8
   uint32_t* keys[2];     // ping-pong; pass i writes buffer i & 1
   uint32_t* perm[2];
   int32_t* d_status;
@@ -180,19 +180,24 @@ __device__ __forceinline__ uint32_t read_rank(const uint32_t* p, uint32_t rank) 
   return v;
 }
 
-// Cluster 0 sorts by least significant digits, each warp owning a contiguous
-// piece of the list; the other clusters clear the outputs meanwhile.
-__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs p) {
-  extern __shared__ uint32_t hist[];  // [warp][digit], then a running position
+// The first CTA (short lists) or cluster sorts by least significant digits, each
+// warp owning a contiguous piece of the list; the other CTAs clear the outputs
+// meanwhile.  A pass is a chain of latencies (count, scan over warps, CTAs and
+// digits, scatter), so it keeps few warps per digit column and its list entries
+// in registers.
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs p) {
+  __shared__ uint32_t hist[kSortWarps][kDigits];  // counts, then running positions
   __shared__ uint32_t total[kDigits], base[kDigits], wsum[kSortWarps];
+  static_assert(kSortThreads == kDigits, "one thread a digit");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x >= kSortCtas) {
-    const int64_t step = (int64_t)(gridDim.x - kSortCtas) * kSortThreads;
-    const int64_t first = (int64_t)(blockIdx.x - kSortCtas) * kSortThreads + tid;
+  if ((int)blockIdx.x >= p.ctas) {
+    const int64_t step = (int64_t)(gridDim.x - p.ctas) * kSortThreads;
+    const int64_t first = (int64_t)(blockIdx.x - p.ctas) * kSortThreads + tid;
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
+#pragma unroll 4
       for (int64_t i = first; i < p.zero_bytes / 16; i += step) p.zero[o][i] = make_uint4(0u, 0u, 0u, 0u);
       uint16_t* tail = reinterpret_cast<uint16_t*>(p.zero[o]);
       for (int64_t i = p.zero_bytes / 16 * 8 + first; i < p.zero_bytes / 2; i += step) tail[i] = 0;
@@ -201,22 +206,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs p)
   }
   if (p.n == 0) return;  // (the whole cluster)
   const uint32_t rank = cluster_rank();
-  const int w = (int)rank * kSortWarps + warp, nw = kSortCtas * kSortWarps;
+  const int w = (int)rank * kSortWarps + warp, nw = p.ctas * kSortWarps;
   const int lo = (int)((int64_t)p.n * w / nw), hi = (int)((int64_t)p.n * (w + 1) / nw);
-  uint32_t* mine = hist + warp * kDigits;
+  uint32_t* mine = hist[warp];
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
     const uint32_t mask = (1u << p.bits) - 1u;
-    const uint32_t* src_k = p.keys[(pass & 1) ^ 1];
-    const uint32_t* src_p = p.perm[(pass & 1) ^ 1];
+    const bool odd = pass & 1, last = pass == p.passes - 1;
+    const uint32_t* src_k = odd ? p.keys[0] : p.keys[1];
+    const uint32_t* src_p = odd ? p.perm[0] : p.perm[1];
+    uint32_t* dst_k = odd ? p.keys[1] : p.keys[0];
+    uint32_t* dst_p = odd ? p.perm[1] : p.perm[0];
     auto key_at = [&](int i) -> uint32_t {
       if (pass) return src_k[i];
       const int32_t id = p.ids[i];
       return id >= 0 && id < p.rows ? (uint32_t)id : (uint32_t)p.rows;  // bad ids come last
     };
-    for (int i = tid; i < kSortWarps * kDigits; i += kSortThreads) hist[i] = 0u;
-    __syncthreads();
-    // (the first kHeld rounds' entries stay in registers for the scatter)
+    // the first kHeld rounds' entries stay in registers for the scatter
     uint32_t hk[kHeld], hp[kHeld];
 #pragma unroll
     for (int r = 0; r < kHeld; ++r) {
@@ -224,30 +230,39 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs p)
       hk[r] = i < hi ? key_at(i) : 0u;
       hp[r] = i < hi ? (pass ? src_p[i] : (uint32_t)i) : 0u;
     }
-    for (int i = lo + lane, r = 0; i < hi; i += 32, ++r) {
-      const uint32_t k = r == 0 ? hk[0] : r == 1 ? hk[1] : key_at(i);
+#pragma unroll
+    for (int j = 0; j < kSortWarps; ++j) hist[j][tid] = 0u;
+    __syncthreads();
+    auto count = [&](uint32_t k) {
       if (pass == 0 && k == (uint32_t)p.rows) set_status(p.d_status, QMM_ERR_BAD_TOKEN_ID);
       atomicAdd(mine + ((k >> shift) & mask), 1u);
-    }
-    __syncthreads();
-    if (tid < kDigits) {  // counts of this CTA's warps -> exclusive prefixes
-      uint32_t run = 0u;
-#pragma unroll 8
-      for (int j = 0; j < kSortWarps; ++j) {
-        const uint32_t c = hist[j * kDigits + tid];
-        hist[j * kDigits + tid] = run;
-        run += c;
-      }
-      total[tid] = run;
-    }
-    cluster_sync();
-    uint32_t before = 0u, all = 0u;
-    if (tid < kDigits) {
+    };
 #pragma unroll
-      for (int r = 0; r < kSortCtas; ++r) {
-        const uint32_t c = read_rank(total + tid, r);
-        before += r < (int)rank ? c : 0u;
-        all += c;
+    for (int r = 0; r < kHeld; ++r)
+      if (lo + 32 * r + lane < hi) count(hk[r]);
+    for (int i = lo + 32 * kHeld + lane; i < hi; i += 32) count(key_at(i));
+    __syncthreads();
+    // counts of this CTA's warps -> exclusive prefixes
+    uint32_t col[kSortWarps], run = 0u;
+#pragma unroll
+    for (int j = 0; j < kSortWarps; ++j) col[j] = hist[j][tid];
+#pragma unroll
+    for (int j = 0; j < kSortWarps; ++j) {
+      hist[j][tid] = run;
+      run += col[j];
+    }
+    uint32_t before = 0u, all = run;
+    if (p.ctas > 1) {
+      total[tid] = run;
+      cluster_sync();
+      uint32_t c[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) c[r] = read_rank(total + tid, r);
+      all = 0u;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        before += r < (int)rank ? c[r] : 0u;
+        all += c[r];
       }
     }
     uint32_t incl = all;  // scan over the digits
@@ -258,31 +273,37 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs p)
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    if (tid < kDigits) {
-      uint32_t off = 0u;
-      for (int j = 0; j < warp; ++j) off += wsum[j];
-      base[tid] = off + incl - all + before;
-    }
+    uint32_t off = 0u;
+#pragma unroll
+    for (int j = 0; j < kSortWarps; ++j) off += j < warp ? wsum[j] : 0u;
+    base[tid] = off + incl - all + before;
     __syncthreads();
-    for (int i0 = lo, rr = 0; i0 < hi; i0 += 32, ++rr) {
-      const int i = i0 + lane;
-      const bool in = i < hi;
+    auto scatter = [&](bool in, uint32_t k, uint32_t t) {
       const uint32_t act = __ballot_sync(0xffffffffu, in);
       if (in) {
-        const uint32_t k = rr == 0 ? hk[0] : rr == 1 ? hk[1] : key_at(i);
-        const uint32_t t = rr == 0 ? hp[0] : rr == 1 ? hp[1] : pass ? src_p[i] : (uint32_t)i;
         const uint32_t d = (k >> shift) & mask;
         const uint32_t peers = __match_any_sync(act, d);
         const int r = __popc(peers & ((1u << lane) - 1u));
         const uint32_t at = base[d] + mine[d] + (uint32_t)r;
         __syncwarp(act);
         if (r == 0) mine[d] += (uint32_t)__popc(peers);
-        p.keys[pass & 1][at] = k;
-        p.perm[pass & 1][at] = t;
+        dst_k[at] = k;
+        dst_p[at] = t;
       }
       __syncwarp();
+    };
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) scatter(lo + 32 * r + lane < hi, hk[r], hp[r]);
+    for (int i0 = lo + 32 * kHeld; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      scatter(in, in ? key_at(i) : 0u, in ? (pass ? src_p[i] : (uint32_t)i) : 0u);
     }
-    cluster_sync();  // the list is whole, and the totals have been read
+    // the list is whole (and the totals have been read)
+    if (p.ctas > 1)
+      cluster_sync();
+    else if (!last)
+      __syncthreads();
   }
 }
 
@@ -390,25 +411,26 @@ __global__ void __launch_bounds__(128) join_kernel(const GradArgs p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int chunk = blockIdx.x, e0 = chunk * p.chunk, last = e0 + p.chunk - 1;
   if (last + 1 >= p.n) return;
-  const uint32_t k = p.keys[last];
-  if (k >= (uint32_t)p.rows || p.keys[last + 1] != k) return;  // no run goes on
-  const bool whole = p.keys[e0] == k;  // it fills this chunk
-  if (whole && e0 > 0 && p.keys[e0 - 1] == k) return;  // it began earlier
-  const int64_t G = p.cols >> p.lgs;
+  const uint32_t k = p.keys[last], first = p.keys[e0], prev = e0 > 0 ? p.keys[e0 - 1] : 0xffffffffu;
   // further chunks that begin with the run, 32 looked at together
+  auto same_at = [&](int from) {
+    const int64_t at = (int64_t)(from + (int)(threadIdx.x & 31)) * p.chunk;
+    return __ballot_sync(0xffffffffu, at < p.n && p.keys[at < p.n ? at : 0] == k);
+  };
+  uint32_t same = same_at(chunk + 1);
+  if (k >= (uint32_t)p.rows || !(same & 1u)) return;  // no run goes on
+  const bool whole = first == k;                      // it fills this chunk
+  if (whole && prev == k) return;                     // it began earlier
+  const int64_t G = p.cols >> p.lgs;
   int pieces = 0;
-  for (;;) {
-    const int64_t at = (int64_t)(chunk + 1 + pieces + (int)(threadIdx.x & 31)) * p.chunk;
-    const uint32_t same = __ballot_sync(0xffffffffu, at < p.n && p.keys[at] == k);
-    if (same != 0xffffffffu) {
-      pieces += __ffs(~same) - 1;
-      break;
-    }
+  while (same == 0xffffffffu) {
     pieces += 32;
+    same = same_at(chunk + 1 + pieces);
   }
+  pieces += __ffs(~same) - 1;
   for (int64_t g = threadIdx.x; g < 2 * G; g += blockDim.x) {
     float sum = p.part[((int64_t)chunk * 2 + (whole ? 0 : 1)) * 2 * G + g];
-#pragma unroll 8
+#pragma unroll 16
     for (int c = 1; c <= pieces; ++c) sum += p.part[(int64_t)(chunk + c) * 4 * G + g];
     store_as(p.out[g >= G], p.g_dtype, (int64_t)k * G + (g >= G ? g - G : g), p.alpha * sum);
   }
@@ -492,18 +514,9 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
   }
   sa.d_status = d_status;
   sa.zero_bytes = w->rows * G * qmm_host::dtype_size((qmm_dtype)g_dtype);
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  constexpr int kSmem = kSortWarps * kDigits * 4;
-  if (!configured[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = 1;
-  }
-  const int sms = qmm_host::num_sms() / kSortCtas * kSortCtas;
-  cudaError_t e = launch_next(sort_kernel, dim3(sms), kSortThreads, kSmem, kSortCtas, sa, st);
+  sa.ctas = n <= 2048 ? 1 : 8;  // (a cluster's barriers cost more than a short list's rounds)
+  const int ctas = qmm_host::num_sms() * 2 / sa.ctas * sa.ctas;
+  cudaError_t e = launch_next(sort_kernel, dim3(ctas), kSortThreads, 0, sa.ctas, sa, st);
   if (e != cudaSuccess || n == 0) return e;
   GradArgs ga{};
   ga.dy = dy;
