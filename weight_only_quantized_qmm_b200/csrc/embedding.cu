@@ -333,9 +333,15 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
   const uint32_t prev = e0 > 0 ? p.keys[e0 - 1] : 0xffffffffu, next = e0 + cnt < p.n ? p.keys[e0 + cnt] : 0xffffffffu;
   const int col = blockIdx.y * kSlab + threadIdx.x * 8;
   const bool live = col < p.cols;  // (threads past the row read its start and store nothing)
-  const TD* dy = reinterpret_cast<const TD*>(p.dy) + (live ? col : 0);
-  const int64_t G = p.cols >> p.lgs;
+  const uint8_t* dy = reinterpret_cast<const uint8_t*>(p.dy) + (live ? col : 0) * (int)sizeof(TD);
+  const uint32_t dy_row = (uint32_t)p.cols * (uint32_t)sizeof(TD), code_row = (uint32_t)(p.cols >> 3) * B;
+  const uint8_t* codes = reinterpret_cast<const uint8_t*>(p.packed) + (int64_t)(col >> 3) * B;
+  const int G = p.cols >> p.lgs, g = col >> p.lgs;
   const int lpg = 1 << (p.lgs - 3);  // threads of a group
+  // after the group's sum, its first thread holds the scale's, its second the bias's
+  const bool odd = threadIdx.x & 1, stores = live && (threadIdx.x & (lpg - 1)) < 2;
+  const uint32_t out_row = (uint32_t)G * (p.g_dtype == QMM_F32 ? 4u : 2u);
+  uint8_t* const out = reinterpret_cast<uint8_t*>(odd ? p.out[1] : p.out[0]) + (int64_t)g * (p.g_dtype == QMM_F32 ? 4 : 2);
   constexpr int U = sizeof(TD) == 4 ? 4 : 8;  // rows requested at a time
   const uint32_t after = __shfl_down_sync(0xffffffffu, key, 1);
   // the entries after which a run or the chunk ends
@@ -352,13 +358,14 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
     for (int j = 0; j < U; ++j) {
       // (lanes past the chunk hold token 0: a valid row, and what a bad id's
       // tokens add is dropped with their run)
-      const int64_t t = __shfl_sync(0xffffffffu, tok, (i0 + j) & 31);
+      const uint32_t t = __shfl_sync(0xffffffffu, tok, (i0 + j) & 31);
+      const uint4* src = reinterpret_cast<const uint4*>(dy + (uint64_t)t * dy_row);
 #pragma unroll
-      for (int h = 0; h < (int)sizeof(TD) / 2; ++h) raw[j][h] = __ldcs(reinterpret_cast<const uint4*>(dy + t * p.cols) + h);
+      for (int h = 0; h < (int)sizeof(TD) / 2; ++h) raw[j][h] = __ldcs(src + h);
       if (ends >> ((i0 + j) & 31) & 1u) {
         const uint32_t k = __shfl_sync(0xffffffffu, key, (i0 + j) & 31);
         if (live && k < (uint32_t)p.rows)
-          load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)k * p.cols + col) / 8 * B, code[j]);
+          load8<B>(codes + (uint64_t)k * code_row, code[j]);
       }
     }
 #pragma unroll
@@ -380,22 +387,16 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
             b2 = add2(b2, acc[c]);
           }
         }
-        float ds = s2.x + s2.y, db = b2.x + b2.y;
-        for (int o = 1; o < lpg; o <<= 1) {
-          ds += __shfl_xor_sync(0xffffffffu, ds, o);
-          db += __shfl_xor_sync(0xffffffffu, db, o);
-        }
-        if (live && (threadIdx.x & (lpg - 1)) == 0) {
-          const int g = col >> p.lgs;
-          const bool open = (start == 0 && prev == k) || (i + 1 == cnt && next == k);
-          if (open) {  // a piece of a longer run
-            float* dst = p.part + ((int64_t)chunk * 2 + (start == 0 ? 0 : 1)) * 2 * G;
-            dst[g] = ds;
-            dst[G + g] = db;
-          } else {
-            store_as(p.out[0], p.g_dtype, (int64_t)k * G + g, p.alpha * ds);
-            store_as(p.out[1], p.g_dtype, (int64_t)k * G + g, p.alpha * db);
-          }
+        const float ds = s2.x + s2.y, db = b2.x + b2.y;
+        float v = (odd ? db : ds) + __shfl_xor_sync(0xffffffffu, odd ? ds : db, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        if (lpg > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
+        if (lpg > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+        if (stores) {
+          if ((start == 0 && prev == k) || (i + 1 == cnt && next == k))  // a piece of a longer run
+            p.part[(((int64_t)chunk * 2 + (start == 0 ? 0 : 1)) * 2 + odd) * G + g] = v;
+          else
+            store_as(out + (uint64_t)k * out_row, p.g_dtype, 0, p.alpha * v);
         }
       }
 #pragma unroll
