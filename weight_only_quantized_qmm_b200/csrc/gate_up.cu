@@ -125,8 +125,8 @@ struct Plan {
 // pair's 256 x 256 tile 0.29 from dense weights and 0.34 dequantizing, a
 // single CTA's 128 x 256 tile 0.62; 2 us to join splits; and for the
 // dequantizing pass 2 us and its bytes at 4.5 TB/s.  Kernels that dequantize want
-// rows of codes on 16 bytes.  A cluster of 8 CTAs finds room on 128 SMs, one of 4
-// on 144.
+// rows of codes on 16 bytes.  Clusters of 4 find room on 132 of the 148 SMs,
+// clusters of 8 on 120 (cudaOccupancyMaxActiveClusters).
 static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits) {
   const int64_t out = op == pg::FWD ? N : K;  // columns of the output
   const int tn = op == pg::FWD ? 128 : 256;
@@ -140,7 +140,7 @@ static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits
     const int64_t mt = ceil_div(M, pair ? 256 : 128), nt = ceil_div(out, tn);
     for (int s = 1; s <= (pair ? 4 : 8); s *= 2) {
       const int ctas = (pair ? 2 : 1) * s;
-      const int room = (ctas >= 8 ? sms * 128 / 148 : ctas >= 4 ? sms * 144 / 148 : sms) / ctas;
+      const int room = (ctas >= 8 ? sms * 120 / 148 : ctas >= 4 ? sms * 132 / 148 : sms) / ctas;
       if (s > 1 && (mt * nt > room || steps < 4 * s)) break;
       const double waves = (double)((mt * nt + room - 1) / room);
       const double c = waves * ceil_div(steps, s) * (dense ? 0.29 : pair ? 0.34 : 0.62) + (s > 1 ? 2.0 : 0.0) +
