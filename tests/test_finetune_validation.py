@@ -44,7 +44,7 @@ def test_embedding_backward(L):
     assert need(10, 100, 128) >= 0 and need(0, 0, 32) >= 0
     assert need(-1, 100, 128) == need(10, -1, 128) == need(10, 100, 0) == need(2 ** 31, 1, 32) == -1
 
-    def call(w=None, dy=A, dy_dtype=BF, ids=A, n=4, ds=A, dz=A, g=BF, ws=A, nb=1 << 40, status=None):
+    def call(w=None, dy=A, dy_dtype=BF, ids=A, n=4000, ds=A, dz=A, g=BF, ws=A, nb=1 << 40, status=None):
         w = w or qw()
         return L.qmm_embedding_backward(dy, dy_dtype, ids, n, ctypes.byref(w), 1.0, ds, dz, g, ws, nb, status, None)
 
@@ -131,7 +131,8 @@ def test_binding():
     refuses("dy has shape", lambda: api.qmm_embedding_backward(z(3, 128), ids, w))
     refuses("dscales", lambda: api.qmm_embedding_backward(z(4, 128), ids, w, dscales=z(31, 2)))
     refuses("dtype", lambda: api.qmm_embedding_backward(z(4, 128), ids, w, dscales=z(32, 2), g_dtype=torch.float32))
-    refuses("workspace", lambda: api.qmm_embedding_backward(z(4, 128), ids, w, workspace=z(1, t=torch.uint8)))
+    refuses("workspace", lambda: api.qmm_embedding_backward(z(4000, 128), z(4000, t=torch.int32), w,
+                                                            workspace=z(1, t=torch.uint8)))
     x, dh = z(3, 128), z(3, 32)
     refuses("CUDA", lambda: api.qmm_gate_up_silu(x, w, w))
     refuses("out holds", lambda: api.qmm_gate_up_silu(x, w, w, out=z(2, 32)))

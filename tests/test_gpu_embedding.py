@@ -109,7 +109,9 @@ def test_gradient(bits, gs, cols, dy_type, g_dtype):
         assert check_grad(dy, some_ids(n, spread, n), qw, 3.5, g_dtype, f"n={n}") == 0
 
 
-@pytest.mark.parametrize("n,rows,kind", [(5000, 70000, "spread"), (4097, 3, "few"), (3000, 1000, "one"),
+@pytest.mark.parametrize("n,rows,kind", [(512, 90000, "spread"), (512, 3, "few"), (500, 77, "one"), (511, 40, "skewed"),
+                                         (513, 90000, "spread"), (1500, 40, "skewed"), (2048, 1, "single row"),
+                                         (5000, 70000, "spread"), (4097, 3, "few"), (3000, 1000, "one"),
                                          (20000, 500, "skewed"), (2049, 1, "single row")])
 def test_gradient_long(n, rows, kind):
     cols = 256

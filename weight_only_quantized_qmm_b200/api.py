@@ -601,14 +601,14 @@ def _structs(call: str, names, tensors, weights):
         if t is not None and t.get_device() != dev:
             here = False
     cs = []
-    for name, w in weights:
-        try:
+    try:
+        for name, w in weights:
             d, c = w.prepared()
-        except ValueError as e:
-            raise ValueError(f"{call}: {name}: {e}") from None
-        if d != dev:
-            here = False
-        cs.append(c)
+            if d != dev:
+                here = False
+            cs.append(c)
+    except ValueError as e:
+        raise ValueError(f"{call}: {name}: {e}") from None
     if not here or dev != torch.cuda.current_device():
         # the slow checks name the tensor that is elsewhere
         _on_device(**dict(zip(names, tensors)))
@@ -690,13 +690,13 @@ def _workspace(call: str, workspace, sizes, like: torch.Tensor, stream):
     return workspace, have
 
 
-def _rows_of(t: torch.Tensor, what: str, cols: int, lead, dtype, stream) -> torch.Tensor:
-    """[..., cols] with leading dimensions `lead`, contiguous."""
-    if t.dim() < 1 or t.shape[-1] != cols or t.shape[:-1] != lead:
-        raise ValueError(f"qmm: {what} has shape {tuple(t.shape)}, expected {(*lead, cols)}")
-    if t.dtype != dtype:
+def _rows_of(t: torch.Tensor, what: str, shape: tuple, dtype, stream) -> torch.Tensor:
+    """`t` of the given shape and dtype, contiguous."""
+    if t.shape != shape:
+        raise ValueError(f"qmm: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"qmm: {what} has dtype {t.dtype}, expected {dtype}")
-    return _dense(t, stream)
+    return t if t.is_contiguous() else _dense(t, stream)
 
 
 def qmm_embedding(ids: torch.Tensor, qw: QWeight, alpha: float = 1.0, y_dtype: torch.dtype | None = None, out=None,
@@ -732,7 +732,7 @@ def qmm_embedding_backward(dy: torch.Tensor, ids: torch.Tensor, qw: QWeight, alp
         _need(d_status, "d_status", 1, _PACKED)
     if qw.mode != QMM_MODE_AFFINE:
         check("qmm_embedding_backward", _lib.QMM_ERR_UNSUPPORTED)
-    dy = _rows_of(dy, "dy", qw.cols, ids.shape, dy.dtype, stream)
+    dy = _rows_of(dy, "dy", (*ids.shape, qw.cols), dy.dtype, stream)
     shape = (qw.rows, _groups(qw.cols, qw.group_size))
     g_dtype = g_dtype or (dscales if dscales is not None else qw.scales).dtype
     dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, dy, stream)
@@ -751,8 +751,8 @@ def qmm_gate_up_silu(x: torch.Tensor, gate: QWeight, up: QWeight, y_dtype: torch
     """h = SiLU(x . dequant(gate)^T) * (x . dequant(up)^T); x [..., K], h [..., F].
     With save (or g_pre and u_pre given) returns (h, g, u), the projections
     in x's dtype that qmm_gate_up_silu_backward reads."""
-    K, F = x.shape[-1], gate.rows
-    shape = (*x.shape[:-1], F)
+    (*lead, K), F = x.shape, gate.rows
+    shape = (*lead, F)
     x2 = _dense(x, stream)
     M = x2.numel() // K if K else 0
     if out is None:
@@ -778,14 +778,19 @@ def qmm_matmul_backward(dy: torch.Tensor, x: torch.Tensor, qw: QWeight, need_dx:
     """Gradients of qmm_matmul(x, qw): (dx, dscales, dbiases), None for what is
     not asked for; dy [..., N], x [..., K], g_dtype x's dtype (default) or
     float32."""
-    lead, K, N, dt = x.shape[:-1], x.shape[-1], qw.rows, x.dtype
+    (*lead, K), N, dt = x.shape, qw.rows, x.dtype
     if K != qw.cols:
         check("qmm_matmul_backward", _lib.QMM_ERR_INVALID_ARG)
     x2 = _dense(x, stream)
-    dy2 = _rows_of(dy, "dy", N, lead, dt, stream)
+    dy2 = _rows_of(dy, "dy", (*lead, N), dt, stream)
     M = x2.numel() // K
     g_dtype = g_dtype or (dscales.dtype if dscales is not None else dt)
-    dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream) if need_dx else None
+    if not need_dx:
+        dx = None
+    elif dx is None and stream is None:
+        dx = torch.empty_like(x2)
+    else:
+        dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream)
     if need_params:
         shape = (N, _groups(K, qw.group_size))
         dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, x2, stream)
@@ -808,16 +813,22 @@ def qmm_gate_up_silu_backward(dh: torch.Tensor, x: torch.Tensor, g_pre: torch.Te
     """Gradients of qmm_gate_up_silu from its saved g_pre and u_pre: (dx,
     (dgate_scales, dgate_biases), (dup_scales, dup_biases)), None for what is
     not asked for; g_dtype is x's dtype (default) or float32."""
-    lead, K, F, dt = x.shape[:-1], x.shape[-1], gate.rows, x.dtype
+    (*lead, K), F, dt = x.shape, gate.rows, x.dtype
+    hidden = (*lead, F)
     if K != gate.cols or K != up.cols or F != up.rows:
         check("qmm_gate_up_silu_backward", _lib.QMM_ERR_INVALID_ARG)
     x2 = _dense(x, stream)
-    dh2 = _rows_of(dh, "dh", F, lead, dt, stream)
-    g2 = _rows_of(g_pre, "g_pre", F, lead, dt, stream)
-    u2 = _rows_of(u_pre, "u_pre", F, lead, dt, stream)
+    dh2 = _rows_of(dh, "dh", hidden, dt, stream)
+    g2 = _rows_of(g_pre, "g_pre", hidden, dt, stream)
+    u2 = _rows_of(u_pre, "u_pre", hidden, dt, stream)
     M = x2.numel() // K
     g_dtype = g_dtype or (dgate[0].dtype if dgate is not None else dt)
-    dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream) if need_dx else None
+    if not need_dx:
+        dx = None
+    elif dx is None and stream is None:
+        dx = torch.empty_like(x2)
+    else:
+        dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream)
     gs = gz = us = uz = None
     if need_params:
         shape = (F, _groups(K, gate.group_size))

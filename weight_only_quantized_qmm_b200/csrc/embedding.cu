@@ -204,7 +204,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     }
     return;
   }
-  if (p.n == 0) return;  // (the whole cluster)
   const uint32_t rank = cluster_rank();
   const int w = (int)rank * kSortWarps + warp, nw = p.ctas * kSortWarps;
   const int lo = (int)((int64_t)p.n * w / nw), hi = (int)((int64_t)p.n * (w + 1) / nw);
@@ -437,6 +436,146 @@ __global__ void __launch_bounds__(128) join_kernel(const GradArgs p) {
   }
 }
 
+// Short lists in one launch, without a sort: a warp takes one token and 256
+// columns, finds the list's entries of the same row by votes, leaves the work to
+// the row's first entry and sums the entries in order; then it folds the
+// groups as grad_kernel does.  Every block also clears the untouched rows of its
+// share of the outputs.  A row with many entries is summed by one warp per 256
+// columns, 16 rows in flight, which is what bounds the list's length.
+constexpr int kShort = 512;
+constexpr int kShortThreads = 256;
+
+struct ShortArgs {
+  const void* dy;
+  const int32_t* ids;
+  const uint32_t* packed;
+  int n, rows, cols, lgs;
+  float alpha;
+  void* out[2];
+  int g_dtype;
+  int32_t* d_status;
+};
+
+template <int B, typename TD>
+__global__ void __launch_bounds__(kShortThreads) short_kernel(const ShortArgs p) {
+  __shared__ int32_t ids[kShort];
+  __shared__ uint32_t touched[1024];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.cols >> p.lgs, esize = p.g_dtype == QMM_F32 ? 4 : 2;
+  // this block's rows to clear, 32768 of them at a time
+  const int r_lo = (int)((int64_t)p.rows * blockIdx.x / gridDim.x), r_hi = (int)((int64_t)p.rows * (blockIdx.x + 1) / gridDim.x);
+  for (int i = tid; i < p.n; i += kShortThreads) {
+    ids[i] = p.ids[i];
+    if (blockIdx.x == 0 && (uint32_t)ids[i] >= (uint32_t)p.rows) set_status(p.d_status, QMM_ERR_BAD_TOKEN_ID);
+  }
+  for (int r0 = r_lo; r0 < r_hi; r0 += 32768) {
+    const int nr = min(32768, r_hi - r0);
+    for (int i = tid; i < (nr + 31) / 32; i += kShortThreads) touched[i] = 0u;
+    __syncthreads();
+    for (int i = tid; i < p.n; i += kShortThreads) {
+      const int64_t r = (int64_t)ids[i] - r0;
+      if (r >= 0 && r < nr) atomicOr(touched + (r >> 5), 1u << (r & 31));
+    }
+    __syncthreads();
+    const int row_bytes = G * esize;
+    const int unit = row_bytes % 16 == 0 ? 16 : esize;
+    const uint32_t per_row = (uint32_t)(row_bytes / unit);
+    const int64_t items = (int64_t)nr * per_row;
+    for (int64_t i = tid; i < items; i += kShortThreads) {
+      const int r = (int)(items <= UINT32_MAX ? (uint32_t)i / per_row : i / per_row);
+      if (touched[r >> 5] >> (r & 31) & 1u) continue;
+      const int64_t at = (int64_t)r0 * row_bytes + i * unit;
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        uint8_t* dst = reinterpret_cast<uint8_t*>(p.out[o]) + at;
+        if (unit == 16)
+          *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        else if (unit == 4)
+          *reinterpret_cast<uint32_t*>(dst) = 0u;
+        else
+          *reinterpret_cast<uint16_t*>(dst) = 0;
+      }
+    }
+    __syncthreads();
+  }
+  __syncthreads();  // (a block without rows to clear)
+  const int slabs = (p.cols + 255) / 256, lpg = 1 << (p.lgs - 3);
+  const int64_t tasks = (int64_t)p.n * slabs;
+  constexpr int U = sizeof(TD) == 4 ? 8 : 16;
+  for (int64_t task = (int64_t)warp * gridDim.x + blockIdx.x; task < tasks;
+       task += (int64_t)gridDim.x * (kShortThreads / 32)) {
+    const int t0 = (int)(task / slabs), slab = (int)(task - (int64_t)t0 * slabs);
+    const int row = ids[t0];
+    if ((uint32_t)row >= (uint32_t)p.rows) continue;
+    // the list as 32-entry masks: lane w keeps that of entries 32 w ..
+    uint32_t mask = 0u;
+    for (int w = 0; w * 32 < p.n; ++w) {
+      const uint32_t m = __ballot_sync(0xffffffffu, w * 32 + lane < p.n && ids[w * 32 + lane] == row);
+      if (lane == w) mask = m;
+    }
+    const uint32_t before = __ballot_sync(0xffffffffu, lane < (t0 >> 5) && mask != 0u);
+    const uint32_t here = __shfl_sync(0xffffffffu, mask, t0 >> 5);
+    if (before != 0u || (here & ((1u << (t0 & 31)) - 1u)) != 0u) continue;  // not its first entry
+    const int col = slab * 256 + lane * 8;
+    const bool live = col < p.cols;
+    const uint8_t* dy = reinterpret_cast<const uint8_t*>(p.dy) + (int64_t)(live ? col : 0) * (int)sizeof(TD);
+    const int64_t dy_row = (int64_t)p.cols * (int)sizeof(TD);
+    uint32_t code[3] = {0u, 0u, 0u};
+    if (live) load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)row * (p.cols >> 3) + (col >> 3)) * B, code);
+    float2 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.0f, 0.0f);
+    int w = t0 >> 5;
+    uint32_t m = here;
+    bool more = true;
+    while (more) {
+      uint4 raw[U][sizeof(TD) / 2];
+      int got = 0;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        while (m == 0u && (w + 1) * 32 < p.n) {
+          ++w;
+          m = __shfl_sync(0xffffffffu, mask, w);
+        }
+        if (m != 0u) {
+          const uint4* src = reinterpret_cast<const uint4*>(dy + (int64_t)(w * 32 + __ffs(m) - 1) * dy_row);
+          m &= m - 1u;
+#pragma unroll
+          for (int h = 0; h < (int)sizeof(TD) / 2; ++h) raw[j][h] = __ldcs(src + h);
+          got = j + 1;
+        }
+      }
+      more = got == U;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (j >= got) break;
+        __align__(16) TD v[8];
+        memcpy(v, raw[j], sizeof(v));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = add2(acc[c], make_float2(to_f32(v[2 * c]), to_f32(v[2 * c + 1])));
+      }
+    }
+    float2 s2 = make_float2(0.0f, 0.0f), b2 = s2;
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s2 = fma2f(acc[c], codes2<B>(code, 2 * c), s2);
+        b2 = add2(b2, acc[c]);
+      }
+    }
+    const bool odd = lane & 1;
+    const float ds = s2.x + s2.y, db = b2.x + b2.y;
+    float v = (odd ? db : ds) + __shfl_xor_sync(0xffffffffu, odd ? ds : db, 1);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    if (lpg > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
+    if (lpg > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+    if (live && (lane & (lpg - 1)) < 2)
+      store_as(odd ? p.out[1] : p.out[0], p.g_dtype, (int64_t)row * G + (col >> p.lgs), p.alpha * v);
+  }
+}
+
 // Tokens of a chunk: up to 32 (one a lane), fewer while that leaves SMs idle.
 static int chunk_of(int64_t n, int64_t cols) {
   const int64_t slabs = (cols + kSlab - 1) / kSlab;
@@ -446,7 +585,8 @@ static int chunk_of(int64_t n, int64_t cols) {
 }
 
 static int64_t grad_workspace(int64_t n, int64_t cols) {
-  const int64_t chunks = (n + 3) / 4 > 0 ? (n + chunk_of(n, cols) - 1) / chunk_of(n, cols) : 0;
+  if (n <= kShort) return 0;
+  const int64_t chunks = (n + chunk_of(n, cols) - 1) / chunk_of(n, cols);
   // two lists of keys and tokens, and the pieces of two runs a chunk (groups of 32 at most)
   return 16 + (n + 3) / 4 * 16 * 4 + chunks * 4 * ((cols + 31) / 32) * 4;
 }
@@ -498,6 +638,19 @@ template <typename TD>
 static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha,
                                void* dscales, void* dbiases, int g_dtype, void* workspace, int32_t* d_status,
                                cudaStream_t st) {
+  if (n <= kShort) {
+    const int lgs = w->group_size == 32 ? 5 : w->group_size == 64 ? 6 : 7;
+    const ShortArgs a{dy, ids, w->packed, (int)n, (int)w->rows, (int)w->cols, lgs, alpha, {dscales, dbiases}, g_dtype,
+                      d_status};
+    const dim3 grid(qmm_host::num_sms() * 8);
+    switch (w->bits) {
+      case 2: return launch_next(short_kernel<2, TD>, grid, kShortThreads, 0, 1, a, st);
+      case 3: return launch_next(short_kernel<3, TD>, grid, kShortThreads, 0, 1, a, st);
+      case 4: return launch_next(short_kernel<4, TD>, grid, kShortThreads, 0, 1, a, st);
+      case 6: return launch_next(short_kernel<6, TD>, grid, kShortThreads, 0, 1, a, st);
+      default: return launch_next(short_kernel<8, TD>, grid, kShortThreads, 0, 1, a, st);
+    }
+  }
   const int64_t G = w->cols / w->group_size, n4 = (n + 3) / 4 * 4;
   uint32_t* ws = static_cast<uint32_t*>(workspace);
   SortArgs sa{};
@@ -518,7 +671,7 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
   sa.ctas = n <= 2048 ? 1 : 8;  // (a cluster's barriers cost more than a short list's rounds)
   const int ctas = qmm_host::num_sms() * 2 / sa.ctas * sa.ctas;
   cudaError_t e = launch_next(sort_kernel, dim3(ctas), kSortThreads, 0, sa.ctas, sa, st);
-  if (e != cudaSuccess || n == 0) return e;
+  if (e != cudaSuccess) return e;
   GradArgs ga{};
   ga.dy = dy;
   ga.keys = sa.keys[(sa.passes - 1) & 1];
@@ -588,7 +741,7 @@ qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int3
   if (d_status && !aligned4(d_status)) return QMM_ERR_ALIGNMENT;
   if (w->rows == 0 && n == 0) return QMM_OK;
   if ((n > 0 && (!aligned16(dy) || !aligned4(ids))) || !aligned16(dscales) || !aligned16(dbiases) ||
-      !aligned16(workspace))
+      (need > 0 && !aligned16(workspace)))
     return QMM_ERR_ALIGNMENT;
   s = qmm_device_check();
   if (s != QMM_OK) return s;

@@ -210,7 +210,10 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
     p.steps = p.parts * ceil_div(N, pg::kBK);
     p.out[0] = dx;
     p.out_dtype = x_dtype;
-    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 128) || !pg::make_map(&tm.a[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 128))
+    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 128)) return cudaErrorInvalidValue;
+    if (!w1)
+      tm.a[1] = tm.a[0];
+    else if (!pg::make_map(&tm.a[1], dy1, p.f16, M, N, ld, 128))
       return cudaErrorInvalidValue;
     tm.b[0] = tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.a[0];
     cudaError_t e = plan.dense ? pg::dequant_parts(pg::DX, w0->bits, p, dense, tm, st) : cudaSuccess;
@@ -223,8 +226,11 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
     p.steps = ceil_div(M, pg::kBK);
     for (int i = 0; i < 4; ++i) p.out[i] = grads[i];
     p.out_dtype = g_dtype;
-    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 64) || !pg::make_map(&tm.a[1], w1 ? dy1 : dy0, p.f16, M, N, ld, 64) ||
-        !pg::make_map(&tm.b[0], x, p.f16, M, K, K, 64))
+    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 64) || !pg::make_map(&tm.b[0], x, p.f16, M, K, K, 64))
+      return cudaErrorInvalidValue;
+    if (!w1)
+      tm.a[1] = tm.a[0];
+    else if (!pg::make_map(&tm.a[1], dy1, p.f16, M, N, ld, 64))
       return cudaErrorInvalidValue;
     tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.b[0];
     return run(pg::DP, w0->bits, plan, p, tm, st);

@@ -1208,7 +1208,7 @@ template <int B>
 cudaError_t dispatch(int op, bool pair, Args& p, Maps& tm, int clusters, cudaStream_t st) {
   if (op == DP) return launch<DP, B, __nv_bfloat16, true>(p, tm, clusters, st);
   p.sb_tma = (p.K >> p.lgs) % 8 == 0;
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < p.parts; ++i)
     if (!(op == FWD ? make_code_maps<FWD, B>(&tm, i, p) : make_code_maps<DX, B>(&tm, i, p))) return cudaErrorNotSupported;
   if (op == FWD) return pair ? launch_t<FWD, B, true>(p, tm, clusters, st) : launch_t<FWD, B, false>(p, tm, clusters, st);
   return pair ? launch_t<DX, B, true>(p, tm, clusters, st) : launch_t<DX, B, false>(p, tm, clusters, st);
