@@ -412,6 +412,8 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
  * the last rounding.  Results do not depend on timing: the same call gives
  * the same bits.
  *
+ * No output overlaps an input, a workspace or another output.
+ *
  * Workspaces are device memory of the caller, 16-byte aligned, of at least
  * the bytes that the matching ..._workspace_bytes call gives (0: NULL will do);
  * a call writes what it reads there, so the contents need no preparation.  Two calls that
@@ -429,7 +431,7 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
 qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha, void* out,
                          qmm_dtype out_dtype, int32_t* d_status, void* stream);
 
-/* Workspace bytes of qmm_embedding_backward (-1 when n is outside [0, 2^31 - 1],
+/* Workspace bytes of qmm_embedding_backward (-1 when n is outside [0, 2^30],
  * rows outside [0, 2^31 - 2] or cols outside [1, 2^25]). */
 int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
 

@@ -126,7 +126,7 @@ def test_binding():
     refuses("dtype", lambda: api.qmm_embedding(ids.long(), w))
     refuses("contiguous", lambda: api.qmm_embedding(z(8, t=torch.int32)[::2], w))
     refuses("expected", lambda: api.qmm_embedding(ids, w, out=z(5, 128)))
-    refuses("out holds", lambda: api.qmm_embedding(ids, w, out=z(3, 128)))
+    refuses("out has shape", lambda: api.qmm_embedding(ids, w, out=z(3, 128)))
     refuses("CUDA", lambda: api.qmm_embedding_backward(z(4, 128), ids, w))
     refuses("dy has shape", lambda: api.qmm_embedding_backward(z(3, 128), ids, w))
     refuses("dscales", lambda: api.qmm_embedding_backward(z(4, 128), ids, w, dscales=z(31, 2)))
@@ -135,7 +135,7 @@ def test_binding():
                                                             workspace=z(1, t=torch.uint8)))
     x, dh = z(3, 128), z(3, 32)
     refuses("CUDA", lambda: api.qmm_gate_up_silu(x, w, w))
-    refuses("out holds", lambda: api.qmm_gate_up_silu(x, w, w, out=z(2, 32)))
+    refuses("out has shape", lambda: api.qmm_gate_up_silu(x, w, w, out=z(2, 32)))
     refuses("g_pre has dtype", lambda: api.qmm_gate_up_silu(x, w, w, g_pre=z(3, 32, t=torch.float32)))
     refuses("CUDA", lambda: api.qmm_matmul_backward(dh, x, w))
     refuses("dy has shape", lambda: api.qmm_matmul_backward(z(3, 31), x, w))

@@ -183,3 +183,29 @@ def test_other_stream_and_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(w, got))
+
+
+def test_offsets_past_32_bits():
+    """A table of 9.8 GB: rows whose codes start past 2^32 bytes, and whose dense
+    index passes 2^33."""
+    rows, cols, gs = 600_000, 16384, 128
+    g = torch.Generator(device=DEV).manual_seed(3)
+    packed = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, cols // 4), dtype=torch.int32, device=DEV, generator=g)
+    scales = torch.rand(rows, cols // gs, device=DEV, generator=g).to(torch.bfloat16)
+    qw = api.QWeight(packed, scales, -scales, rows, cols, gs, 8)
+    ids = torch.tensor([rows - 1, 0, 599_123, rows - 1, 262_144, 300_001], dtype=torch.int32, device=DEV)
+    u, where = torch.unique(ids.long(), return_inverse=True)
+    small = api.QWeight(packed[u].contiguous(), scales[u].contiguous(), -scales[u].contiguous(), u.numel(), cols, gs, 8)
+    _, W = p64.dequant64(small)
+    want = W[where] * 2.0
+    bound = 2 * p64.U[torch.float32] * want.abs()
+    p64.close(api.qmm_embedding(ids, qw, 2.0, torch.float32), want, p64.rounded(bound, want, torch.float32), "lookup")
+    for n in (ids.numel(), 900):  # both ways the list is taken
+        many = ids.repeat(-(-n // ids.numel()))[:n].contiguous()
+        dy = (wl.gen_x(n, 512, 4).to(DEV) * 0.1).repeat(1, cols // 512)
+        ds, dz = api.qmm_embedding_backward(dy, many, qw, 2.0, g_dtype=torch.float32)
+        w = where.repeat(-(-n // ids.numel()))[:n].to(torch.int32)
+        wants, bounds = grad64(dy, w, small, 2.0)
+        for got, wt, b in zip((ds, dz), wants, bounds):
+            p64.close(got[u], wt, p64.rounded(b, wt, torch.float32), f"gradient n={n}")
+            assert int((got.abs().sum(1) > 0).sum()) == u.numel()

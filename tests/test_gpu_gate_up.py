@@ -226,3 +226,11 @@ def test_other_stream_and_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(w, got))
+
+
+def test_wide_and_tall_weights():
+    """Long sums, one column of tiles, and rows past many tiles."""
+    check_matmul_backward(40, 2, 128, 16384, 70, BF, F32)
+    check_forward(33, 2, 128, 16384, 70, BF)
+    check_matmul_backward(20, 4, 32, 64, 20000, HF, F32)
+    check_forward(150, 4, 32, 64, 20000, HF)

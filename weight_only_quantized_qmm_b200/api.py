@@ -654,21 +654,20 @@ def _exactly(t, what: str, shape, dtypes, like: torch.Tensor, stream) -> torch.T
     a new one of the first dtype."""
     if t is None:
         return _new(shape, dtypes[0], like, stream)
-    n = 1
-    for d in shape:
-        n *= d
-    _need(t, what, n, dtypes)
-    if t.numel() != n:
-        raise ValueError(f"qmm: {what} holds {t.numel()} elements, expected {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"qmm: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _need(t, what, 0, dtypes)
     return t
 
 
-def _grads(given, names, shape, dtype, like: torch.Tensor, stream):
-    """The parameter gradients `given`, checked, or new ones (in one piece of
-    memory where each starts on 16 bytes)."""
-    if any(t is not None for t in given) or (shape[0] * shape[1] * dtype.itemsize) % 16:
-        return [_exactly(t, n, shape, (dtype,), like, stream) for t, n in zip(given, names)]
-    return _new((len(names), *shape), dtype, like, stream).unbind(0)
+def _grads(given, names, shape, dtype, w: QWeight, stream):
+    """The parameter gradients `given`, checked, or new ones (shaped as the
+    weight's scales)."""
+    like = w.scales
+    if stream is None and like.dtype is dtype and like.shape == shape:
+        return [torch.empty_like(like) if t is None else _exactly(t, n, shape, (dtype,), like, None)
+                for t, n in zip(given, names)]
+    return [_exactly(t, n, shape, (dtype,), like, stream) for t, n in zip(given, names)]
 
 
 @functools.lru_cache(maxsize=1024)
@@ -683,7 +682,9 @@ def _workspace(call: str, workspace, sizes, like: torch.Tensor, stream):
     """(workspace or None, its bytes)"""
     need = _workspace_bytes(call, *sizes)
     if workspace is None:
-        return (None if need == 0 else _new((need,), torch.uint8, like, stream)), need
+        if need == 0:
+            return None, 0
+        return _new((-(-need // like.element_size()),), like.dtype, like, stream), need
     have = workspace.numel() * workspace.element_size()
     if not workspace.is_contiguous() or have < need:
         raise ValueError(f"{call}: workspace must be contiguous and hold at least {need} bytes")
@@ -711,7 +712,7 @@ def qmm_embedding(ids: torch.Tensor, qw: QWeight, alpha: float = 1.0, y_dtype: t
         _need(d_status, "d_status", 1, _PACKED)
     if out is None:
         dt = y_dtype or (qw.scales.dtype if qw.mode == QMM_MODE_AFFINE else torch.float32)
-        out = _new((*ids.shape, qw.cols), dt, ids, stream)
+        out = _new((*ids.shape, qw.cols), dt, qw.scales if ids.is_cuda else ids, stream)
     else:
         out = _exactly(out, "out", (*ids.shape, qw.cols), _FLOAT, ids, stream)
     dev, (c,) = _structs("qmm_embedding", ("ids", "out", "d_status"), (ids, out, d_status), (("table", qw),))
@@ -735,7 +736,7 @@ def qmm_embedding_backward(dy: torch.Tensor, ids: torch.Tensor, qw: QWeight, alp
     dy = _rows_of(dy, "dy", (*ids.shape, qw.cols), dy.dtype, stream)
     shape = (qw.rows, _groups(qw.cols, qw.group_size))
     g_dtype = g_dtype or (dscales if dscales is not None else qw.scales).dtype
-    dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, dy, stream)
+    dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, qw, stream)
     ws, nbytes = _workspace("qmm_embedding_backward", workspace, (n, qw.rows, qw.cols), dy, stream)
     dev, (c,) = _structs("qmm_embedding_backward", ("dy", "ids", "dscales", "dbiases", "workspace", "d_status"),
                          (dy, ids, dscales, dbiases, ws, d_status), (("table", qw),))
@@ -793,7 +794,7 @@ def qmm_matmul_backward(dy: torch.Tensor, x: torch.Tensor, qw: QWeight, need_dx:
         dx = _exactly(dx, "dx", x.shape, (dt,), x2, stream)
     if need_params:
         shape = (N, _groups(K, qw.group_size))
-        dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, x2, stream)
+        dscales, dbiases = _grads((dscales, dbiases), ("dscales", "dbiases"), shape, g_dtype, qw, stream)
     else:
         dscales = dbiases = None
     ws, nbytes = _workspace("qmm_matmul_backward", workspace, (M, K, N, qw.bits), x2, stream)
@@ -833,7 +834,7 @@ def qmm_gate_up_silu_backward(dh: torch.Tensor, x: torch.Tensor, g_pre: torch.Te
     if need_params:
         shape = (F, _groups(K, gate.group_size))
         gs, gz, us, uz = _grads((*(dgate or (None, None)), *(dup or (None, None))),
-                                ("dgate_scales", "dgate_biases", "dup_scales", "dup_biases"), shape, g_dtype, x2,
+                                ("dgate_scales", "dgate_biases", "dup_scales", "dup_biases"), shape, g_dtype, gate,
                                 stream)
     ws, nbytes = _workspace("qmm_gate_up_silu_backward", workspace, (M, K, F, gate.bits), x2, stream)
     dev, (cg, cu) = _structs(

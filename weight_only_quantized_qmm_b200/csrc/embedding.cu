@@ -723,7 +723,7 @@ qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, fl
 }
 
 int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t cols) {
-  if (n < 0 || n > (int64_t)INT32_MAX || rows < 0 || rows >= (int64_t)INT32_MAX || cols <= 0 ||
+  if (n < 0 || n > (1 << 30) || rows < 0 || rows >= (int64_t)INT32_MAX || cols <= 0 ||
       cols > (1 << 25))
     return -1;
   return qmm::embed::grad_workspace(n, cols);

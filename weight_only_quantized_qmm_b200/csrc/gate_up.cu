@@ -330,7 +330,7 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
   if ((dscales == nullptr) != (dbiases == nullptr) || (!dx && !dscales)) return QMM_ERR_INVALID_ARG;
   const int64_t need = qmm_matmul_backward_workspace_bytes(M, K, w->rows, w->bits);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
-  if (M > 0 && w->rows > 0 && (!aligned16(dy) || !aligned16(x))) return QMM_ERR_ALIGNMENT;
+  if (M > 0 && w->rows > 0 && (!aligned16(dy) || (dscales && !aligned16(x)))) return QMM_ERR_ALIGNMENT;
   if ((dx && !aligned16(dx)) || (dscales && (!aligned16(dscales) || !aligned16(dbiases))) ||
       (need > 0 && !aligned16(workspace)))
     return QMM_ERR_ALIGNMENT;
@@ -371,7 +371,7 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
   const int64_t F = gate->rows;
   const int64_t need = qmm_gate_up_silu_backward_workspace_bytes(M, K, F, gate->bits);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
-  if (M > 0 && F > 0 && (!aligned16(dh) || !aligned16(x) || !aligned16(g_pre) || !aligned16(u_pre)))
+  if (M > 0 && F > 0 && (!aligned16(dh) || (grads[0] && !aligned16(x)) || !aligned16(g_pre) || !aligned16(u_pre)))
     return QMM_ERR_ALIGNMENT;
   if ((dx && !aligned16(dx)) || (need > 0 && !aligned16(workspace))) return QMM_ERR_ALIGNMENT;
   for (int i = 0; i < 4; ++i)
