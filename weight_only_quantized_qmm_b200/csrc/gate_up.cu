@@ -23,6 +23,11 @@ cudaError_t dispatch_b3(int, bool, Args&, Maps&, int, cudaStream_t);
 cudaError_t dispatch_b4(int, bool, Args&, Maps&, int, cudaStream_t);
 cudaError_t dispatch_b6(int, bool, Args&, Maps&, int, cudaStream_t);
 cudaError_t dispatch_b8(int, bool, Args&, Maps&, int, cudaStream_t);
+cudaError_t dispatch_both_b2(Args&, Maps&, const Args&, const Maps&, int, int, cudaStream_t);
+cudaError_t dispatch_both_b3(Args&, Maps&, const Args&, const Maps&, int, int, cudaStream_t);
+cudaError_t dispatch_both_b4(Args&, Maps&, const Args&, const Maps&, int, int, cudaStream_t);
+cudaError_t dispatch_both_b6(Args&, Maps&, const Args&, const Maps&, int, int, cudaStream_t);
+cudaError_t dispatch_both_b8(Args&, Maps&, const Args&, const Maps&, int, int, cudaStream_t);
 cudaError_t dispatch_dense(int, const Args&, const Maps&, int, cudaStream_t);
 cudaError_t dequant_parts(int op, int bits, const Args& p, void* ws, Maps& tm, cudaStream_t st);
 }  // namespace pg
@@ -125,7 +130,8 @@ struct Plan {
 // pair's 256 x 256 tile 0.29 from dense weights and 0.34 dequantizing, a
 // single CTA's 128 x 256 tile 0.62; 2 us to join splits; and for the
 // dequantizing pass 2 us and its bytes at 4.5 TB/s.  Kernels that dequantize want
-// rows of codes on 16 bytes.  Clusters of 4 find room on 132 of the 148 SMs,
+// rows of codes on 16 bytes; dx runs on pairs only, which shares a launch with the
+// parameter gradients.  Clusters of 4 find room on 132 of the 148 SMs,
 // clusters of 8 on 120 (cudaOccupancyMaxActiveClusters).
 static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits) {
   const int64_t out = op == pg::FWD ? N : K;  // columns of the output
@@ -134,7 +140,7 @@ static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits
   const int sms = qmm_host::num_sms();
   Plan best{};
   double cost = 1e300;
-  for (int kind = 0; kind < 3; ++kind) {
+  for (int kind = 0; kind < (op == pg::FWD ? 3 : 2); ++kind) {
     const bool dense = kind == 0, pair = kind < 2;
     if (!dense && (K * bits) % 128 != 0) continue;
     const int64_t mt = ceil_div(M, pair ? 256 : 128), nt = ceil_div(out, tn);
@@ -203,39 +209,65 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
     for (int i = 0; i < (w1 ? 4 : 2) && grads[0] && bytes && e == cudaSuccess; ++i) e = cudaMemsetAsync(grads[i], 0, bytes, st);
     return e;
   }
-  pg::Maps tm;
+  pg::Args a = args_of(M, K, w0, w1, x_dtype), g = a;  // dx, parameter gradients
+  pg::Maps am, gm;
+  Plan plan{};
   if (dx) {
-    pg::Args p = args_of(M, K, w0, w1, x_dtype);
-    const Plan plan = plan_of(pg::DX, M, K, N, p.parts, w0->bits);
-    p.steps = p.parts * ceil_div(N, pg::kBK);
-    p.out[0] = dx;
-    p.out_dtype = x_dtype;
-    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 128)) return cudaErrorInvalidValue;
+    plan = plan_of(pg::DX, M, K, N, a.parts, w0->bits);
+    a.steps = a.parts * ceil_div(N, pg::kBK);
+    a.out[0] = dx;
+    a.out_dtype = x_dtype;
+    if (!pg::make_map(&am.a[0], dy0, a.f16, M, N, ld, 128)) return cudaErrorInvalidValue;
     if (!w1)
-      tm.a[1] = tm.a[0];
-    else if (!pg::make_map(&tm.a[1], dy1, p.f16, M, N, ld, 128))
+      am.a[1] = am.a[0];
+    else if (!pg::make_map(&am.a[1], dy1, a.f16, M, N, ld, 128))
       return cudaErrorInvalidValue;
-    tm.b[0] = tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.a[0];
-    cudaError_t e = plan.dense ? pg::dequant_parts(pg::DX, w0->bits, p, dense, tm, st) : cudaSuccess;
-    if (e == cudaSuccess) e = run(pg::DX, plan.dense ? 0 : w0->bits, plan, p, tm, st);
+    am.b[0] = am.b[1] = am.s[0] = am.s[1] = am.z[0] = am.z[1] = am.a[0];
+  }
+  const Plan gplan{true, true, 1, ceil_div(N, 256), ceil_div(K, 256)};
+  if (grads[0]) {
+    g.steps = ceil_div(M, pg::kBK);
+    for (int i = 0; i < 4; ++i) g.out[i] = grads[i];
+    g.out_dtype = g_dtype;
+    if (!pg::make_map(&gm.a[0], dy0, g.f16, M, N, ld, 64) || !pg::make_map(&gm.b[0], x, g.f16, M, K, K, 64))
+      return cudaErrorInvalidValue;
+    if (!w1)
+      gm.a[1] = gm.a[0];
+    else if (!pg::make_map(&gm.a[1], dy1, g.f16, M, N, ld, 64))
+      return cudaErrorInvalidValue;
+    gm.b[1] = gm.s[0] = gm.s[1] = gm.z[0] = gm.z[1] = gm.b[0];
+  }
+  const int sms = qmm_host::num_sms();
+  const int64_t tiles = (int64_t)plan.m_tiles * plan.n_tiles, gtiles = (int64_t)gplan.m_tiles * gplan.n_tiles * g.parts;
+  const int pairs = (plan.splits == 4 ? sms * 120 / 148 : plan.splits == 2 ? sms * 132 / 148 : sms) / 2;
+  if (dx && grads[0] && !plan.dense && tiles * plan.splits <= pairs - pairs / 4) {
+    // one launch: the parameter gradients take the pairs that dx leaves (64 tokens
+    // of 4096 x 14336: 138 us against 104 + 66; where dx leaves less than a quarter
+    // of the SMs, two launches are as fast: 1024 tokens 497 us against 250 + 220)
+    a.m_tiles = plan.m_tiles;
+    a.n_tiles = plan.n_tiles;
+    a.splits = plan.splits;
+    g.m_tiles = gplan.m_tiles;
+    g.n_tiles = gplan.n_tiles;
+    g.splits = 1;
+    const int clusters = (int)tiles;
+    int gpairs = (int)std::min<int64_t>(gtiles, pairs - clusters * plan.splits);
+    gpairs = (gpairs + plan.splits - 1) / plan.splits * plan.splits;
+    if (gtiles > INT32_MAX / 16) return cudaErrorInvalidValue;
+    switch (w0->bits) {
+      case 2: return pg::dispatch_both_b2(a, am, g, gm, clusters, gpairs, st);
+      case 3: return pg::dispatch_both_b3(a, am, g, gm, clusters, gpairs, st);
+      case 4: return pg::dispatch_both_b4(a, am, g, gm, clusters, gpairs, st);
+      case 6: return pg::dispatch_both_b6(a, am, g, gm, clusters, gpairs, st);
+      default: return pg::dispatch_both_b8(a, am, g, gm, clusters, gpairs, st);
+    }
+  }
+  if (dx) {
+    cudaError_t e = plan.dense ? pg::dequant_parts(pg::DX, w0->bits, a, dense, am, st) : cudaSuccess;
+    if (e == cudaSuccess) e = run(pg::DX, plan.dense ? 0 : w0->bits, plan, a, am, st);
     if (e != cudaSuccess) return e;
   }
-  if (grads[0]) {
-    pg::Args p = args_of(M, K, w0, w1, x_dtype);
-    const Plan plan{true, true, 1, ceil_div(N, 256), ceil_div(K, 256)};
-    p.steps = ceil_div(M, pg::kBK);
-    for (int i = 0; i < 4; ++i) p.out[i] = grads[i];
-    p.out_dtype = g_dtype;
-    if (!pg::make_map(&tm.a[0], dy0, p.f16, M, N, ld, 64) || !pg::make_map(&tm.b[0], x, p.f16, M, K, K, 64))
-      return cudaErrorInvalidValue;
-    if (!w1)
-      tm.a[1] = tm.a[0];
-    else if (!pg::make_map(&tm.a[1], dy1, p.f16, M, N, ld, 64))
-      return cudaErrorInvalidValue;
-    tm.b[1] = tm.s[0] = tm.s[1] = tm.z[0] = tm.z[1] = tm.b[0];
-    return run(pg::DP, w0->bits, plan, p, tm, st);
-  }
-  return cudaSuccess;
+  return grads[0] ? run(pg::DP, w0->bits, gplan, g, gm, st) : cudaSuccess;
 }
 
 static int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }

@@ -16,8 +16,8 @@
 // PAIR: two CTAs share one 256 x 256 tile (cta_group::2); each holds 128 rows
 // of A and half of B, so an SM reads and writes 64 KB of shared memory per
 // 64-deep step (512 tensor cycles) instead of the 96 KB of a 128 x 256 tile,
-// which is what bounds that tile.  Single: one CTA per 128 x 256 tile for few
-// tokens.  Where the tiles are few, a cluster of `splits` CTAs (or pairs) shares
+// which is what bounds that tile.  Single (FWD): one CTA per 128 x 256 tile for
+// few tokens.  Where the tiles are few, a cluster of `splits` CTAs (or pairs) shares
 // one by cutting the sum, and joins its partial tiles through distributed shared
 // memory in rank order.
 //
@@ -94,7 +94,7 @@ struct Cfg {
   static constexpr int BAR0 = WIN0 + (DENSE ? 0 : 2 * WINDOW);
   static constexpr int BARS = 2 * STAGES + 5 + 2 * SLOTS + 2;
   static constexpr int SMEM = 1024 + BAR0 + 512;                   // + alignment slack, barriers
-  static_assert(!DENSE || PAIR, "these run on CTA pairs");
+  static_assert((!DENSE && OP == FWD) || PAIR, "these run on CTA pairs");
   static_assert(DENSE || SLOTS >= 3, "room for the codes");
   static_assert(8 * BARS + 8 <= 512, "barriers, TMEM slot and abort flag");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -511,9 +511,10 @@ __device__ __forceinline__ void store_h8(const Args& p, int m, int n, const floa
   }
 }
 
+// One product by `blocks` CTAs, of which this is number `block`; at least
+// Cfg::THREADS threads (warps past those only keep the barriers).
 template <int OP, int B, typename T, bool PAIR>
-__global__ void __launch_bounds__(Cfg<OP, B, PAIR>::THREADS, 1)
-pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm) {
+__device__ __forceinline__ void product(const Args& p, const Maps& tm, int block, int blocks) {
   using C = Cfg<OP, B, PAIR>;
   constexpr int S = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -537,8 +538,8 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
   const bool leader = side == 0;
   const int splits = p.splits;
   const int cta_per = (PAIR ? 2 : 1) * splits;  // CTAs of a cluster
-  const int cluster = blockIdx.x / cta_per, clusters = gridDim.x / cta_per;
-  const int split = PAIR ? (int)(rank >> 1) : (int)rank;
+  const int cluster = block / cta_per, clusters = blocks / cta_per;
+  const int split = splits == 1 ? 0 : PAIR ? (int)(rank >> 1) : (int)rank;
   // this CTA's range of steps, and its cluster's tiles
   const int s_lo = (int)((int64_t)p.steps * split / splits), s_hi = (int)((int64_t)p.steps * (split + 1) / splits);
   const int nk = s_hi - s_lo;
@@ -679,7 +680,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
       for (uint32_t i = 0; i < kPolls && !poll(drain, 0); ++i) {
       }
     }
-  } else if (!C::DENSE && warp >= 2 + C::EPI) {
+  } else if (!C::DENSE && warp >= 2 + C::EPI && warp < C::THREADS / 32) {
    if constexpr (!C::DENSE) {
     const int half = p.steps / p.parts;    // DX: steps of one part
     const int spw = p.lgs - 3;             // log2 of the steps of a window: 8 groups
@@ -865,7 +866,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
   // The epilogue warps; where each CTA has one tile, the dequant warps too once
   // they are done (a tile's columns are dealt out 16 at a time).
   const bool only = T_all <= clusters;
-  if ((warp >= 2 && warp < 2 + C::EPI) || (!C::DENSE && only && warp > 2 + C::EPI)) {
+  if ((warp >= 2 && warp < 2 + C::EPI) || (!C::DENSE && only && warp > 2 + C::EPI && warp < C::THREADS / 32)) {
     constexpr int kEach = C::EPI / 4 + C::DEQ / 4;  // warps of a lane quarter, when all take part
     const int first = (C::DENSE || !only || warp < 2 + C::EPI) ? 0 : 16 * (1 + (warp - 3 - C::EPI) / 4);
     const int stride = (C::DENSE || !only) ? 16 : 16 * kEach;
@@ -1082,7 +1083,7 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
       const int per = COLS / 8 / splits;  // 8-column pieces of this CTA (splits divides 16)
       const bool vec = OP == DX || p.N % 8 == 0;
       const int m0 = tl.m0 + 128 * side, rows = min(128, p.M - m0);
-      for (int it = threadIdx.x; it < per * 128; it += C::THREADS) {
+      for (int it = threadIdx.x; it < per * 128; it += (int)blockDim.x) {
         const int row = it & 127, c = (split * per + (it >> 7)) * 8;
         if (row >= rows || tl.n0 + c >= (OP == FWD ? p.N : p.K)) continue;
         float v[2][8];
@@ -1114,6 +1115,26 @@ pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
+}
+
+template <int OP, int B, typename T, bool PAIR>
+__global__ void __launch_bounds__(Cfg<OP, B, PAIR>::THREADS, 1)
+pair_gemm_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps tm) {
+  product<OP, B, T, PAIR>(p, tm, (int)blockIdx.x, (int)gridDim.x);
+}
+
+// Both products of a backward pass in one launch: the first dx_blocks CTAs take
+// dx, the others the parameter gradients, so that few tiles of the one leave no
+// SM idle that the other can use.  (Both use cta_group::2, as one kernel must.)
+template <int B, typename T>
+__global__ void __launch_bounds__(Cfg<DX, B, true>::THREADS, 1)
+backward_kernel(const __grid_constant__ Args dx, const __grid_constant__ Maps dx_maps, const __grid_constant__ Args dp,
+                const __grid_constant__ Maps dp_maps, int dx_blocks) {
+  static_assert(Cfg<DX, B, true>::THREADS >= Cfg<DP, B, true>::THREADS, "one block shape for both");
+  if ((int)blockIdx.x < dx_blocks)
+    product<DX, B, T, true>(dx, dx_maps, (int)blockIdx.x, dx_blocks);
+  else
+    product<DP, B, T, true>(dp, dp_maps, (int)blockIdx.x - dx_blocks, (int)gridDim.x - dx_blocks);
 }
 
 // ------------------------------------------------------------------ host
@@ -1166,24 +1187,23 @@ bool make_code_maps(Maps* tm, int part, const Args& p) {
   return true;
 }
 
-template <int OP, int B, typename T, bool PAIR>
-cudaError_t launch(const Args& p, const Maps& tm, int clusters, cudaStream_t st) {
-  using C = Cfg<OP, B, PAIR>;
-  auto k = pair_gemm_kernel<OP, B, T, PAIR>;
-  static int configured[64] = {0};
+// A launch of `blocks` CTAs in clusters of `per`, programmatic after the
+// previous kernel; the shared-memory limit is raised once per device and kernel.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*k)(P...), int* configured, int blocks, int threads, int smem, int per, cudaStream_t st,
+                          const A&... args) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
-  const int per = (PAIR ? 2 : 1) * p.splits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * per);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1193,7 +1213,15 @@ cudaError_t launch(const Args& p, const Maps& tm, int clusters, cudaStream_t st)
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = per > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, p, tm);
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <int OP, int B, typename T, bool PAIR>
+cudaError_t launch(const Args& p, const Maps& tm, int clusters, cudaStream_t st) {
+  using C = Cfg<OP, B, PAIR>;
+  static int configured[64] = {0};
+  const int per = (PAIR ? 2 : 1) * p.splits;
+  return launch_kernel(pair_gemm_kernel<OP, B, T, PAIR>, configured, clusters * per, C::THREADS, C::SMEM, per, st, p, tm);
 }
 
 template <int OP, int B, bool PAIR>
@@ -1210,8 +1238,27 @@ cudaError_t dispatch(int op, bool pair, Args& p, Maps& tm, int clusters, cudaStr
   p.sb_tma = (p.K >> p.lgs) % 8 == 0;
   for (int i = 0; i < p.parts; ++i)
     if (!(op == FWD ? make_code_maps<FWD, B>(&tm, i, p) : make_code_maps<DX, B>(&tm, i, p))) return cudaErrorNotSupported;
-  if (op == FWD) return pair ? launch_t<FWD, B, true>(p, tm, clusters, st) : launch_t<FWD, B, false>(p, tm, clusters, st);
-  return pair ? launch_t<DX, B, true>(p, tm, clusters, st) : launch_t<DX, B, false>(p, tm, clusters, st);
+  if (op == DX) return launch_t<DX, B, true>(p, tm, clusters, st);
+  return pair ? launch_t<FWD, B, true>(p, tm, clusters, st) : launch_t<FWD, B, false>(p, tm, clusters, st);
+}
+
+// Both products of a backward pass in one launch.  dx_clusters of dx, then
+// dp_pairs CTA pairs (a multiple of dx.splits) of the parameter gradients.
+template <int B>
+cudaError_t dispatch_both(Args& dx, Maps& dx_maps, const Args& dp, const Maps& dp_maps, int dx_clusters, int dp_pairs,
+                          cudaStream_t st) {
+  dx.sb_tma = (dx.K >> dx.lgs) % 8 == 0;
+  for (int i = 0; i < dx.parts; ++i)
+    if (!make_code_maps<DX, B>(&dx_maps, i, dx)) return cudaErrorNotSupported;
+  constexpr int kThreads = Cfg<DX, B, true>::THREADS;
+  constexpr int kSmem = std::max(Cfg<DX, B, true>::SMEM, Cfg<DP, B, true>::SMEM);
+  static int configured[2][64] = {{0}};
+  const int per = 2 * dx.splits, dx_blocks = dx_clusters * per, blocks = dx_blocks + 2 * dp_pairs;
+  if (dx.f16)
+    return launch_kernel(backward_kernel<B, __half>, configured[0], blocks, kThreads, kSmem, per, st, dx, dx_maps, dp,
+                         dp_maps, dx_blocks);
+  return launch_kernel(backward_kernel<B, __nv_bfloat16>, configured[1], blocks, kThreads, kSmem, per, st, dx, dx_maps,
+                       dp, dp_maps, dx_blocks);
 }
 
 }  // namespace pg

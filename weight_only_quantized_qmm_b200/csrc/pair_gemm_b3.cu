@@ -8,5 +8,10 @@ cudaError_t dispatch_b3(int op, bool pair, Args& p, Maps& tm, int clusters, cuda
   return dispatch<3>(op, pair, p, tm, clusters, st);
 }
 
+cudaError_t dispatch_both_b3(Args& dx, Maps& dx_maps, const Args& dp, const Maps& dp_maps, int dx_clusters,
+                             int dp_pairs, cudaStream_t st) {
+  return dispatch_both<3>(dx, dx_maps, dp, dp_maps, dx_clusters, dp_pairs, st);
+}
+
 }  // namespace pg
 }  // namespace qmm
