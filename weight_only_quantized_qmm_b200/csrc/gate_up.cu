@@ -126,13 +126,13 @@ struct Plan {
   int m_tiles, n_tiles;
 };
 
-// The cheapest by the times measured for one 64-deep step (us, 4096 x 14336): a
-// pair's 256 x 256 tile 0.29 from dense weights and 0.34 dequantizing, a
-// single CTA's 128 x 256 tile 0.62; 2 us to join splits; and for the
+// The cheapest by the times measured for one 64-deep step (us, 4096 x 14336, 4
+// bits): a pair's 256 x 256 tile 0.39 from dense weights and 0.45 dequantizing,
+// a single CTA's 128 x 256 tile 0.66; 3 us to join splits; and for the
 // dequantizing pass 2 us and its bytes at 4.5 TB/s.  Kernels that dequantize want
 // rows of codes on 16 bytes; dx runs on pairs only, which shares a launch with the
-// parameter gradients.  Clusters of 4 find room on 132 of the 148 SMs,
-// clusters of 8 on 120 (cudaOccupancyMaxActiveClusters).
+// parameter gradients.  Clusters of 4 find room on 132 of the 148 SMs, clusters
+// of 8 on 120 (cudaOccupancyMaxActiveClusters).
 static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits) {
   const int64_t out = op == pg::FWD ? N : K;  // columns of the output
   const int tn = op == pg::FWD ? 128 : 256;
@@ -149,7 +149,7 @@ static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits
       const int room = (ctas >= 8 ? sms * 120 / 148 : ctas >= 4 ? sms * 132 / 148 : sms) / ctas;
       if (s > 1 && (mt * nt > room || steps < 4 * s)) break;
       const double waves = (double)((mt * nt + room - 1) / room);
-      const double c = waves * ceil_div(steps, s) * (dense ? 0.29 : pair ? 0.34 : 0.62) + (s > 1 ? 2.0 : 0.0) +
+      const double c = waves * ceil_div(steps, s) * (dense ? 0.39 : pair ? 0.45 : 0.66) + (s > 1 ? 3.0 : 0.0) +
                        (dense ? 2.0 + (double)parts * N * K * (2.0 + bits / 8.0) / 4.5e6 : 0.0);
       if (c < cost) {
         cost = c;

@@ -840,10 +840,17 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
         li += SETS;
         if (li >= nk) settle();
         if (!p.sb_tma) fetch(sn, zn);
+        // all of the unit before the wait for its stage, which the MMAs of S steps
+        // ago hold: what then stands between them and the next is the store alone
+        uint4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q] = dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3);
+          asm volatile("" ::"r"(v[q].x), "r"(v[q].y), "r"(v[q].z), "r"(v[q].w));
+        }
         if (u > 0) wait_fast(empty0 + 8 * s, (u - 1) & 1, abort_flag);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          sts_v4(dst ^ (uint32_t)(q << 4), dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3));
+        for (int q = 0; q < 8; ++q) sts_v4(dst ^ (uint32_t)(q << 4), v[q]);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
         __syncwarp();
         if (lane == 0) {
