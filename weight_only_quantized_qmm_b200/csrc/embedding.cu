@@ -441,9 +441,9 @@ __global__ void __launch_bounds__(128) join_kernel(const GradArgs p) {
 // the row's first entry and sums the entries in order; then it folds the
 // groups as grad_kernel does.  Every block also clears the untouched rows of its
 // share of the outputs.  A row with many entries is summed by one warp per 256
-// columns, 16 rows in flight, which is what bounds the list's length.
+// columns, 8 rows in flight, which is what bounds the list's length.
 constexpr int kShort = 512;
-constexpr int kShortThreads = 256;
+constexpr int kShortThreads = 256, kShortBlocks = 4;  // per SM: one wave
 
 struct ShortArgs {
   const void* dy;
@@ -457,7 +457,7 @@ struct ShortArgs {
 };
 
 template <int B, typename TD>
-__global__ void __launch_bounds__(kShortThreads) short_kernel(const ShortArgs p) {
+__global__ void __launch_bounds__(kShortThreads, kShortBlocks) short_kernel(const ShortArgs p) {
   __shared__ int32_t ids[kShort];
   __shared__ uint32_t touched[1024];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kShortThreads) short_kernel(const ShortArgs p)
   __syncthreads();  // (a block without rows to clear)
   const int slabs = (p.cols + 255) / 256, lpg = 1 << (p.lgs - 3);
   const int64_t tasks = (int64_t)p.n * slabs;
-  constexpr int U = sizeof(TD) == 4 ? 8 : 16;
+  constexpr int U = sizeof(TD) == 4 ? 4 : 8;
   for (int64_t task = (int64_t)warp * gridDim.x + blockIdx.x; task < tasks;
        task += (int64_t)gridDim.x * (kShortThreads / 32)) {
     const int t0 = (int)(task / slabs), slab = (int)(task - (int64_t)t0 * slabs);
@@ -642,7 +642,7 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
     const int lgs = w->group_size == 32 ? 5 : w->group_size == 64 ? 6 : 7;
     const ShortArgs a{dy, ids, w->packed, (int)n, (int)w->rows, (int)w->cols, lgs, alpha, {dscales, dbiases}, g_dtype,
                       d_status};
-    const dim3 grid(qmm_host::num_sms() * 8);
+    const dim3 grid(qmm_host::num_sms() * kShortBlocks);
     switch (w->bits) {
       case 2: return launch_next(short_kernel<2, TD>, grid, kShortThreads, 0, 1, a, st);
       case 3: return launch_next(short_kernel<3, TD>, grid, kShortThreads, 0, 1, a, st);
