@@ -234,3 +234,97 @@ def test_wide_and_tall_weights():
     check_forward(33, 2, 128, 16384, 70, BF)
     check_matmul_backward(20, 4, 32, 64, 20000, HF, F32)
     check_forward(150, 4, 32, 64, 20000, HF)
+
+
+def test_two_streams_and_two_graphs_at_once():
+    """Calls that overlap on the GPU share nothing: two streams, and two captured
+    graphs replayed on two streams, give the bits of calls by themselves."""
+    K, F = 1024, 640
+    gate, up = weight(F, K, 4, 64, BF, 1), weight(F, K, 4, 64, BF, 2)
+    sizes = (40, 300, 1700)
+    data = [(act(m, K, m, BF), act(m, F, m + 1, BF)) for m in sizes]
+
+    def step(x, dh, stream=None):
+        h, g, u = api.qmm_gate_up_silu(x, gate, up, save=True, stream=stream)
+        dx, dg, du = api.qmm_gate_up_silu_backward(dh, x, g, u, gate, up, stream=stream)
+        return [h, g, u, dx, *dg, *du, *api.qmm_matmul_backward(dh, x, gate, stream=stream)]
+
+    want = [step(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    for _ in range(5):
+        got = [step(*d, stream=s) for d, s in zip(data, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
+    graphs, outs = [], []
+    for d in data:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(*d))
+    for o in outs:
+        for t in o:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, g in zip(want, outs) for a, b in zip(w, g))
+
+
+def test_rows_after_the_last_token_are_left():
+    """Outputs given with more memory behind them: nothing past the call's rows is
+    written (odd row lengths, every path)."""
+    K, F, gs = 256, 77, 32
+    gate, up = weight(F, K, 6, gs, HF, 1), weight(F, K, 6, gs, HF, 2)
+    for M in (1, 9, 31, 140, 600):
+        x = act(M, K, M, HF)
+        g = [Guarded((M, F), HF) for _ in range(3)]
+        api.qmm_gate_up_silu(x, gate, up, out=g[0].out, g_pre=g[1].out, u_pre=g[2].out)
+        dx = Guarded((M, K), HF)
+        p = [Guarded((F, K // gs), F32) for _ in range(4)]
+        api.qmm_gate_up_silu_backward(act(M, F, 5, HF), x, g[1].out, g[2].out, gate, up, dx=dx.out,
+                                      dgate=(p[0].out, p[1].out), dup=(p[2].out, p[3].out))
+        torch.cuda.synchronize()
+        for i, t in enumerate((*g, dx, *p)):
+            t.check(f"M={M} output {i}")
+
+
+def test_large_scales_and_zero_weights():
+    """Values at the ends of the type: weights of 1e30 in bf16, groups whose scale
+    and bias are zero, and codes at both ends."""
+    M, K, F, gs = 70, 128, 96, 64
+    gate = weight(F, K, 4, gs, BF, 1)
+    up = weight(F, K, 4, gs, BF, 2)
+    gate.scales[3], gate.biases[3] = 0.0, 0.0
+    gate.packed[5], gate.packed[6] = 0, -1
+    up.scales[7] = 1e30
+    up.biases[7] = -1e30
+    x = act(M, K, 3, BF)
+    (h, g, u), (eh, eg, eu) = p64.gate_up64(x, gate, up, BF)
+    hh, gg, uu = api.qmm_gate_up_silu(x, gate, up, save=True)
+    for got, w, e in ((gg, g, eg), (uu, u, eu)):
+        err = (got.double() - w).abs()
+        assert (err <= p64.rounded(e, w, BF)).all()
+    err = (hh.double() - h).abs()
+    assert (err <= p64.rounded(eh, h, BF)).all()
+    assert (gg[:, 3] == 0).all() and (hh[:, 3] == 0).all()
+    dy = act(M, F, 4, BF)
+    dy[:, 7] = 0  # the row of 1e30 adds nothing
+    dx, ds, dz = api.qmm_matmul_backward(dy, x, up)
+    want, bound = p64.dx64([dy.double()], [up], F32, BF)
+    assert torch.isfinite(dx).all() and ((dx.double() - want).abs() <= p64.rounded(bound, want, BF)).all()
+    assert (ds[7] == 0).all() and (dz[7] == 0).all()
+
+
+@pytest.mark.parametrize("bits,gs,K,N", [(4, 32, 512, 200), (8, 128, 2048, 150), (3, 32, 1280, 333), (6, 32, 1024, 90),
+                                         (2, 64, 1024, 700), (3, 128, 2048, 70), (8, 32, 1536, 129), (2, 32, 1056, 64),
+                                         (3, 32, 1440, 700), (6, 64, 1600, 257)])
+@pytest.mark.parametrize("M", [50, 200])
+def test_scale_windows_and_split_sums(M, bits, gs, K, N):
+    """Rows of scales that come by TMA (a multiple of 8 groups) at every width and
+    group size, rows of codes off 16 bytes, and sums cut over clusters."""
+    check_forward(M, bits, gs, K, N, BF)
+    check_matmul_backward(M, bits, gs, K, N, HF, F32)
+    check_gated_backward(M, bits, gs, K, N, BF, BF)

@@ -16,11 +16,10 @@ namespace qmm {
 namespace embed {
 
 template <typename K, typename A>
-static cudaError_t launch_next(K kernel, dim3 grid, int threads, size_t smem, int cluster, const A& args, cudaStream_t st) {
+static cudaError_t launch_next(K kernel, dim3 grid, int threads, int cluster, const A& args, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -340,7 +339,8 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
   // after the group's sum, its first thread holds the scale's, its second the bias's
   const bool odd = threadIdx.x & 1, stores = live && (threadIdx.x & (lpg - 1)) < 2;
   const uint32_t out_row = (uint32_t)G * (p.g_dtype == QMM_F32 ? 4u : 2u);
-  uint8_t* const out = reinterpret_cast<uint8_t*>(odd ? p.out[1] : p.out[0]) + (int64_t)g * (p.g_dtype == QMM_F32 ? 4 : 2);
+  uint8_t* const out =
+      reinterpret_cast<uint8_t*>(odd ? p.out[1] : p.out[0]) + (int64_t)g * (p.g_dtype == QMM_F32 ? 4 : 2);
   constexpr int U = sizeof(TD) == 4 ? 4 : 8;  // rows requested at a time
   const uint32_t after = __shfl_down_sync(0xffffffffu, key, 1);
   // the entries after which a run or the chunk ends
@@ -465,7 +465,8 @@ __global__ void __launch_bounds__(kShortThreads, kShortBlocks) short_kernel(cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.cols >> p.lgs, esize = p.g_dtype == QMM_F32 ? 4 : 2;
   // this block's rows to clear, 32768 of them at a time
-  const int r_lo = (int)((int64_t)p.rows * blockIdx.x / gridDim.x), r_hi = (int)((int64_t)p.rows * (blockIdx.x + 1) / gridDim.x);
+  const int r_lo = (int)((int64_t)p.rows * blockIdx.x / gridDim.x);
+  const int r_hi = (int)((int64_t)p.rows * (blockIdx.x + 1) / gridDim.x);
   for (int i = tid; i < p.n; i += kShortThreads) {
     ids[i] = p.ids[i];
     if (blockIdx.x == 0 && (uint32_t)ids[i] >= (uint32_t)p.rows) set_status(p.d_status, QMM_ERR_BAD_TOKEN_ID);
@@ -523,7 +524,8 @@ __global__ void __launch_bounds__(kShortThreads, kShortBlocks) short_kernel(cons
     const uint8_t* dy = reinterpret_cast<const uint8_t*>(p.dy) + (int64_t)(live ? col : 0) * (int)sizeof(TD);
     const int64_t dy_row = (int64_t)p.cols * (int)sizeof(TD);
     uint32_t code[3] = {0u, 0u, 0u};
-    if (live) load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + ((int64_t)row * (p.cols >> 3) + (col >> 3)) * B, code);
+    const int64_t piece = (int64_t)row * (p.cols >> 3) + (col >> 3);
+    if (live) load8<B>(reinterpret_cast<const uint8_t*>(p.packed) + piece * B, code);
     float2 acc[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.0f, 0.0f);
@@ -594,8 +596,8 @@ static int64_t grad_workspace(int64_t n, int64_t cols) {
 template <int B, int MODE, typename TS>
 static cudaError_t lookup_o(const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha, void* out, int out_dtype,
                             int32_t* d_status, cudaStream_t st) {
-  LookArgs a{ids, w->packed, w->scales, w->biases, (int)std::min<int64_t>(w->rows, INT32_MAX), (int)n, (int)(w->cols / 8), 4, kLookThreads, alpha, out,
-             d_status};
+  const int rows = (int)std::min<int64_t>(w->rows, INT32_MAX);  // ids are 32-bit
+  LookArgs a{ids, w->packed, w->scales, w->biases, rows, (int)n, (int)(w->cols / 8), 4, kLookThreads, alpha, out, d_status};
   while ((1 << a.lgs) < w->group_size) ++a.lgs;  // 16 (nvfp4), 32, 64 or 128
   while (a.lanes / 2 >= a.pieces) a.lanes /= 2;
   const int per_block = kLookThreads / a.lanes;
@@ -604,9 +606,10 @@ static cudaError_t lookup_o(const int32_t* ids, int64_t n, const qmm_qweight* w,
   const int64_t want = (n + per_block - 1) / per_block;
   const int64_t most = std::max<int64_t>(1, (int64_t)qmm_host::num_sms() * 16 / tiles);
   const dim3 grid((unsigned)std::min(want, most), (unsigned)tiles);
-  if (out_dtype == QMM_F32) return launch_next(lookup_kernel<B, MODE, TS, float>, grid, kLookThreads, 0, 1, a, st);
-  if (out_dtype == QMM_BF16) return launch_next(lookup_kernel<B, MODE, TS, __nv_bfloat16>, grid, kLookThreads, 0, 1, a, st);
-  return launch_next(lookup_kernel<B, MODE, TS, __half>, grid, kLookThreads, 0, 1, a, st);
+  constexpr int kThreads = kLookThreads;
+  if (out_dtype == QMM_F32) return launch_next(lookup_kernel<B, MODE, TS, float>, grid, kThreads, 1, a, st);
+  if (out_dtype == QMM_BF16) return launch_next(lookup_kernel<B, MODE, TS, __nv_bfloat16>, grid, kThreads, 1, a, st);
+  return launch_next(lookup_kernel<B, MODE, TS, __half>, grid, kThreads, 1, a, st);
 }
 
 template <int B>
@@ -644,11 +647,11 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
                       d_status};
     const dim3 grid(qmm_host::num_sms() * kShortBlocks);
     switch (w->bits) {
-      case 2: return launch_next(short_kernel<2, TD>, grid, kShortThreads, 0, 1, a, st);
-      case 3: return launch_next(short_kernel<3, TD>, grid, kShortThreads, 0, 1, a, st);
-      case 4: return launch_next(short_kernel<4, TD>, grid, kShortThreads, 0, 1, a, st);
-      case 6: return launch_next(short_kernel<6, TD>, grid, kShortThreads, 0, 1, a, st);
-      default: return launch_next(short_kernel<8, TD>, grid, kShortThreads, 0, 1, a, st);
+      case 2: return launch_next(short_kernel<2, TD>, grid, kShortThreads, 1, a, st);
+      case 3: return launch_next(short_kernel<3, TD>, grid, kShortThreads, 1, a, st);
+      case 4: return launch_next(short_kernel<4, TD>, grid, kShortThreads, 1, a, st);
+      case 6: return launch_next(short_kernel<6, TD>, grid, kShortThreads, 1, a, st);
+      default: return launch_next(short_kernel<8, TD>, grid, kShortThreads, 1, a, st);
     }
   }
   const int64_t G = w->cols / w->group_size, n4 = (n + 3) / 4 * 4;
@@ -670,7 +673,7 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
   sa.zero_bytes = w->rows * G * qmm_host::dtype_size((qmm_dtype)g_dtype);
   sa.ctas = n <= 2048 ? 1 : 8;  // (a cluster's barriers cost more than a short list's rounds)
   const int ctas = qmm_host::num_sms() * 2 / sa.ctas * sa.ctas;
-  cudaError_t e = launch_next(sort_kernel, dim3(ctas), kSortThreads, 0, sa.ctas, sa, st);
+  cudaError_t e = launch_next(sort_kernel, dim3(ctas), kSortThreads, sa.ctas, sa, st);
   if (e != cudaSuccess) return e;
   GradArgs ga{};
   ga.dy = dy;
@@ -690,14 +693,14 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
   ga.part = reinterpret_cast<float*>(ws + 4 * n4);
   const dim3 grid(ga.chunks, (unsigned)((w->cols + kSlab - 1) / kSlab));
   switch (w->bits) {
-    case 2: e = launch_next(grad_kernel<2, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
-    case 3: e = launch_next(grad_kernel<3, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
-    case 4: e = launch_next(grad_kernel<4, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
-    case 6: e = launch_next(grad_kernel<6, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
-    default: e = launch_next(grad_kernel<8, TD>, grid, kSlabThreads, 0, 1, ga, st); break;
+    case 2: e = launch_next(grad_kernel<2, TD>, grid, kSlabThreads, 1, ga, st); break;
+    case 3: e = launch_next(grad_kernel<3, TD>, grid, kSlabThreads, 1, ga, st); break;
+    case 4: e = launch_next(grad_kernel<4, TD>, grid, kSlabThreads, 1, ga, st); break;
+    case 6: e = launch_next(grad_kernel<6, TD>, grid, kSlabThreads, 1, ga, st); break;
+    default: e = launch_next(grad_kernel<8, TD>, grid, kSlabThreads, 1, ga, st); break;
   }
   if (e != cudaSuccess || ga.chunks == 1) return e;
-  return launch_next(join_kernel, dim3(ga.chunks - 1), 128, 0, 1, ga, st);
+  return launch_next(join_kernel, dim3(ga.chunks - 1), 128, 1, ga, st);
 }
 
 }  // namespace embed

@@ -206,7 +206,8 @@ static cudaError_t backward(const void* dy0, const void* dy1, int64_t ld, const 
     cudaError_t e = cudaSuccess;
     if (dx && M > 0) e = cudaMemsetAsync(dx, 0, (size_t)(M * K * 2), st);
     const size_t bytes = (size_t)(N * (K / w0->group_size) * qmm_host::dtype_size((qmm_dtype)g_dtype));
-    for (int i = 0; i < (w1 ? 4 : 2) && grads[0] && bytes && e == cudaSuccess; ++i) e = cudaMemsetAsync(grads[i], 0, bytes, st);
+    for (int i = 0; i < (w1 ? 4 : 2) && grads[0] && bytes && e == cudaSuccess; ++i)
+      e = cudaMemsetAsync(grads[i], 0, bytes, st);
     return e;
   }
   pg::Args a = args_of(M, K, w0, w1, x_dtype), g = a;  // dx, parameter gradients

@@ -643,7 +643,11 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0 && leader) {
+    if (PAIR && lane == 0 && !leader) {
+      // (the leader's last commit arrives here too: nothing is on its way after it)
+      for (uint32_t i = 0; i < kPolls && !poll(drain, 0); ++i) {
+      }
+    } else if (lane == 0) {
       constexpr bool AMN = OP == DP, BMN = OP != FWD;
       constexpr int AK = AMN ? 2048 : 32, BK_ = BMN ? 2048 : 32;  // bytes per 16 k
       const uint32_t fmt = p.f16 ? 0u : 1u;
@@ -681,192 +685,191 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
       }
     }
   } else if (!C::DENSE && warp >= 2 + C::EPI && warp < C::THREADS / 32) {
-   if constexpr (!C::DENSE) {
-    const int half = p.steps / p.parts;    // DX: steps of one part
-    const int spw = p.lgs - 3;             // log2 of the steps of a window: 8 groups
-    if (warp == 2 + C::EPI) {
-      // ---------------- producer of the codes, scales and biases ----------------
-      if (lane == 0) {
-        const uint32_t sb_tx = p.sb_tma ? 2 * C::SB : 0;
-        int j = 0, done = 0, win = 0, win_start = 0;  // done: steps known to be dequantized
-        bool stop = false;
-        auto reach = [&](int upto) {
-          for (; done < upto; ++done)
-            if (!wait(cempty0 + 8 * (done % C::SLOTS), (done / C::SLOTS) & 1, abort_flag))
-              return false;
-          return true;
-        };
-        for (int lt = 0; lt < my_tiles && !stop; ++lt) {
-          const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
-          for (int i = s_lo; i < s_hi; ++i, ++j) {
-            if (OP == FWD && p.sb_tma && (i == s_lo || (i & ((1 << spw) - 1)) == 0)) {
-              // the window before the last one makes room
-              if (!reach(win_start)) {
+    if constexpr (!C::DENSE) {
+      const int half = p.steps / p.parts;    // DX: steps of one part
+      const int spw = p.lgs - 3;             // log2 of the steps of a window: 8 groups
+      if (warp == 2 + C::EPI) {
+        // ---------------- producer of the codes, scales and biases ----------------
+        if (lane == 0) {
+          const uint32_t sb_tx = p.sb_tma ? 2 * C::SB : 0;
+          int j = 0, done = 0, win = 0, win_start = 0;  // done: steps known to be dequantized
+          bool stop = false;
+          auto reach = [&](int upto) {
+            for (; done < upto; ++done)
+              if (!wait(cempty0 + 8 * (done % C::SLOTS), (done / C::SLOTS) & 1, abort_flag)) return false;
+            return true;
+          };
+          for (int lt = 0; lt < my_tiles && !stop; ++lt) {
+            const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
+            for (int i = s_lo; i < s_hi; ++i, ++j) {
+              if (OP == FWD && p.sb_tma && (i == s_lo || (i & ((1 << spw) - 1)) == 0)) {
+                // the window before the last one makes room
+                if (!reach(win_start)) {
+                  stop = true;
+                  break;
+                }
+                const uint32_t d = stage0 + C::WIN0 + (win & 1) * C::WINDOW, bar = wfull0 + 8 * (win & 1);
+                const int g = ((i * kBK) >> p.lgs) & ~7;
+                mbar_arrive_expect_tx(bar, C::WINDOW);
+#pragma unroll
+                for (int x = 0; x < C::BOXES; ++x) {
+                  const int part = PAIR ? side : x;
+                  tma_2d<false>(d + (2 * x) * C::SB, &tm.s[part], g, tl.n0, bar);
+                  tma_2d<false>(d + (2 * x + 1) * C::SB, &tm.z[part], g, tl.n0, bar);
+                }
+                ++win;
+                win_start = j;
+              }
+              if (!reach(j - C::SLOTS + 1)) {
                 stop = true;
                 break;
               }
-              const uint32_t d = stage0 + C::WIN0 + (win & 1) * C::WINDOW, bar = wfull0 + 8 * (win & 1);
-              const int g = ((i * kBK) >> p.lgs) & ~7;
-              mbar_arrive_expect_tx(bar, C::WINDOW);
+              const uint32_t d = stage0 + C::CODE0 + (j % C::SLOTS) * C::SLOT, bar = cfull0 + 8 * (j % C::SLOTS);
+              mbar_arrive_expect_tx(bar, C::BOXES * C::BOX + (OP == DX ? sb_tx : 0u));
+              if constexpr (OP == FWD) {
+                const int w = B == 3 ? (i >> 1) * 12 : i * 2 * B;  // first word
 #pragma unroll
-              for (int x = 0; x < C::BOXES; ++x) {
-                const int part = PAIR ? side : x;
-                tma_2d<false>(d + (2 * x) * C::SB, &tm.s[part], g, tl.n0, bar);
-                tma_2d<false>(d + (2 * x + 1) * C::SB, &tm.z[part], g, tl.n0, bar);
-              }
-              ++win;
-              win_start = j;
-            }
-            if (!reach(j - C::SLOTS + 1)) {
-              stop = true;
-              break;
-            }
-            const uint32_t d = stage0 + C::CODE0 + (j % C::SLOTS) * C::SLOT, bar = cfull0 + 8 * (j % C::SLOTS);
-            mbar_arrive_expect_tx(bar, C::BOXES * C::BOX + (OP == DX ? sb_tx : 0u));
-            if constexpr (OP == FWD) {
-              const int w = B == 3 ? (i >> 1) * 12 : i * 2 * B;  // first word
+                for (int x = 0; x < C::BOXES; ++x)
+                  tma_2d<false>(d + x * C::BOX, &tm.b[PAIR ? side : x], w, tl.n0, bar);
+              } else {
+                const int part = i >= half, n = (part ? i - half : i) * kBK;
+                const int col = tl.n0 + 128 * side;
 #pragma unroll
-              for (int x = 0; x < C::BOXES; ++x)
-                tma_2d<false>(d + x * C::BOX, &tm.b[PAIR ? side : x], w, tl.n0, bar);
-            } else {
-              const int part = i >= half, n = (part ? i - half : i) * kBK;
-              const int col = tl.n0 + 128 * side;
-#pragma unroll
-              for (int x = 0; x < C::BOXES; ++x)
-                tma_2d<false>(d + x * C::BOX, &tm.b[part], ((col + 128 * x) >> 5) * B, n, bar);
-              if (p.sb_tma) {
-                const int g = (col >> p.lgs) & ~7;
-                tma_2d<false>(d + C::BOXES * C::BOX, &tm.s[part], g, n, bar);
-                tma_2d<false>(d + C::BOXES * C::BOX + C::SB, &tm.z[part], g, n, bar);
+                for (int x = 0; x < C::BOXES; ++x)
+                  tma_2d<false>(d + x * C::BOX, &tm.b[part], ((col + 128 * x) >> 5) * B, n, bar);
+                if (p.sb_tma) {
+                  const int g = (col >> p.lgs) & ~7;
+                  tma_2d<false>(d + C::BOXES * C::BOX, &tm.s[part], g, n, bar);
+                  tma_2d<false>(d + C::BOXES * C::BOX + C::SB, &tm.z[part], g, n, bar);
+                }
               }
             }
           }
-        }
-        if (stop) {
-          // (as the other producer: copies may be landing)
-          *abort_flag = 1;
-          for (int q = max(0, j - C::SLOTS); q < j; ++q)
-            mbar_wait_n(cfull0 + 8 * (q % C::SLOTS), (q / C::SLOTS) & 1, 1u << 12);
-          for (int q = max(0, win - 2); q < win; ++q) mbar_wait_n(wfull0 + 8 * (q & 1), (q >> 1) & 1, 1u << 12);
-        }
-      }
-    } else {
-      // ---------------- dequantize ----------------
-      // the sets of warps that fill a stage (PAIR: 128 rows of B, 4 warps;
-      // single: 256, 8 warps) take turns
-      constexpr int WPS = PAIR ? 4 : 8, SETS = kDeqWarps / WPS;
-      const int dw = warp - 3 - C::EPI, set = dw / WPS;
-      const uint32_t lfull0 = PAIR ? map_rank(full0, lead) : full0;
-      // this thread's 128 bytes of the operand tile: FWD, row r of B; DX, row
-      // r of the step's 64 in block blk of 64 columns.  16-byte pieces are
-      // swizzled by the row, so eight lanes write eight bank groups.
-      const int r = OP == FWD ? (dw % WPS) * 32 + lane : (dw & 1) * 32 + lane;
-      const int blk = OP == FWD ? 0 : (dw % WPS) >> 1;
-      const uint32_t at = C::A_BYTES + (uint32_t)(blk * 8192 + r * 128);
-      const int swz = r & 7;
-      // its codes in a slot, its scales in a window or slot
-      const int crow = OP == FWD ? r & 127 : r, cbox = OP == FWD ? r >> 7 : blk >> 1;
-      const uint32_t codes = stage0 + C::CODE0 + (uint32_t)(cbox * C::BOX + crow * C::ROW);
-      const int cswz = C::swz(crow);
-      const uint32_t sbs = OP == FWD ? stage0 + C::WIN0 + (uint32_t)(2 * cbox * C::SB + crow * 16)
-                                     : stage0 + C::CODE0 + (uint32_t)(C::BOXES * C::BOX + crow * 16);
-      const int nwin = ((s_hi - 1) >> spw) - (s_lo >> spw) + 1;  // windows of a tile
-      const int total = my_tiles * nk;
-      const int64_t G = p.K >> p.lgs;
-      int li = set, lt = 0, n0 = 0;
-      auto settle = [&]() {  // li to a step of tile lt
-        while (li >= nk) li -= nk, ++lt;
-        n0 = lt < my_tiles ? tile_of<OP, PAIR>(p, cluster + lt * clusters).n0 : 0;
-      };
-      // first column of the unit's 64 codes and its two halves' groups
-      auto column = [&]() {
-        return OP == FWD ? (s_lo + li) * kBK : n0 + 128 * side + blk * 64;
-      };
-      // scales and biases of the unit at the cursor, from global memory
-      auto fetch = [&](uint16_t (&sv)[2], uint16_t (&zv)[2]) {
-        const int i = s_lo + li, k = column();
-        int row, part;
-        if constexpr (OP == FWD) {
-          part = PAIR ? side : r >> 7;
-          row = n0 + (r & 127);
-        } else {
-          part = i >= half;
-          row = (part ? i - half : i) * kBK + r;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kh = k + 32 * h;
-          sv[h] = zv[h] = 0;
-          if (lt < my_tiles && row < p.N && kh < p.K) {  // past the weight: zeros
-            const int64_t g = row * G + (kh >> p.lgs);
-            sv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].scales) + g);
-            zv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].biases) + g);
+          if (stop) {
+            // (as the other producer: copies may be landing)
+            *abort_flag = 1;
+            for (int q = max(0, j - C::SLOTS); q < j; ++q)
+              mbar_wait_n(cfull0 + 8 * (q % C::SLOTS), (q / C::SLOTS) & 1, 1u << 12);
+            for (int q = max(0, win - 2); q < win; ++q) mbar_wait_n(wfull0 + 8 * (q & 1), (q >> 1) & 1, 1u << 12);
           }
         }
-      };
-      uint16_t sn[2] = {0, 0}, zn[2] = {0, 0};
-      if (total > 0) settle();
-      if (!p.sb_tma && total > 0) fetch(sn, zn);
-      int s = set % S, u = set / S, c = set % C::SLOTS, cu = set / C::SLOTS;
-      uint32_t dst = stage0 + (uint32_t)(s * C::STAGE) + at + (uint32_t)(swz << 4);
-      uint32_t src = codes + (uint32_t)(c * C::SLOT);
-      int win_in = -1;  // FWD: the last window waited for
-      for (int j = set; j < total; j += SETS) {
-        const int i = s_lo + li, k = column();
-        uint32_t w[2][B];
-        uint16_t sv[2], zv[2];
-        wait_fast(cfull0 + 8 * c, cu & 1, abort_flag);
-        read_codes<B>(src, OP == FWD ? (B == 3 ? (i & 1) * 24 : 0) : (blk & 1) * 8 * B, cswz, w);
-        if (p.sb_tma) {
-          uint32_t o = sbs + ((k >> p.lgs) & 7) * 2;
+      } else {
+        // ---------------- dequantize ----------------
+        // the sets of warps that fill a stage (PAIR: 128 rows of B, 4 warps;
+        // single: 256, 8 warps) take turns
+        constexpr int WPS = PAIR ? 4 : 8, SETS = kDeqWarps / WPS;
+        const int dw = warp - 3 - C::EPI, set = dw / WPS;
+        const uint32_t lfull0 = PAIR ? map_rank(full0, lead) : full0;
+        // this thread's 128 bytes of the operand tile: FWD, row r of B; DX, row
+        // r of the step's 64 in block blk of 64 columns.  16-byte pieces are
+        // swizzled by the row, so eight lanes write eight bank groups.
+        const int r = OP == FWD ? (dw % WPS) * 32 + lane : (dw & 1) * 32 + lane;
+        const int blk = OP == FWD ? 0 : (dw % WPS) >> 1;
+        const uint32_t at = C::A_BYTES + (uint32_t)(blk * 8192 + r * 128);
+        const int swz = r & 7;
+        // its codes in a slot, its scales in a window or slot
+        const int crow = OP == FWD ? r & 127 : r, cbox = OP == FWD ? r >> 7 : blk >> 1;
+        const uint32_t codes = stage0 + C::CODE0 + (uint32_t)(cbox * C::BOX + crow * C::ROW);
+        const int cswz = C::swz(crow);
+        const uint32_t sbs = OP == FWD ? stage0 + C::WIN0 + (uint32_t)(2 * cbox * C::SB + crow * 16)
+                                       : stage0 + C::CODE0 + (uint32_t)(C::BOXES * C::BOX + crow * 16);
+        const int nwin = ((s_hi - 1) >> spw) - (s_lo >> spw) + 1;  // windows of a tile
+        const int total = my_tiles * nk;
+        const int64_t G = p.K >> p.lgs;
+        int li = set, lt = 0, n0 = 0;
+        auto settle = [&]() {  // li to a step of tile lt
+          while (li >= nk) li -= nk, ++lt;
+          n0 = lt < my_tiles ? tile_of<OP, PAIR>(p, cluster + lt * clusters).n0 : 0;
+        };
+        // first column of the unit's 64 codes and its two halves' groups
+        auto column = [&]() {
+          return OP == FWD ? (s_lo + li) * kBK : n0 + 128 * side + blk * 64;
+        };
+        // scales and biases of the unit at the cursor, from global memory
+        auto fetch = [&](uint16_t (&sv)[2], uint16_t (&zv)[2]) {
+          const int i = s_lo + li, k = column();
+          int row, part;
           if constexpr (OP == FWD) {
-            const int win = lt * nwin + (i >> spw) - (s_lo >> spw);
-            if (win != win_in) wait_fast(wfull0 + 8 * (win & 1), (win >> 1) & 1, abort_flag);
-            win_in = win;
-            o += (uint32_t)((win & 1) * C::WINDOW);
+            part = PAIR ? side : r >> 7;
+            row = n0 + (r & 127);
           } else {
-            o += (uint32_t)(c * C::SLOT);
+            part = i >= half;
+            row = (part ? i - half : i) * kBK + r;
           }
-          sv[0] = sv[1] = lds_u16(o);
-          zv[0] = zv[1] = lds_u16(o + C::SB);
-          if (p.lgs == 5) {  // 64 codes are two groups
-            sv[1] = lds_u16(o + 2);
-            zv[1] = lds_u16(o + C::SB + 2);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int kh = k + 32 * h;
+            sv[h] = zv[h] = 0;
+            if (lt < my_tiles && row < p.N && kh < p.K) {  // past the weight: zeros
+              const int64_t g = row * G + (kh >> p.lgs);
+              sv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].scales) + g);
+              zv[h] = __ldg(reinterpret_cast<const uint16_t*>(p.w[part].biases) + g);
+            }
           }
-        } else {
+        };
+        uint16_t sn[2] = {0, 0}, zn[2] = {0, 0};
+        if (total > 0) settle();
+        if (!p.sb_tma && total > 0) fetch(sn, zn);
+        int s = set % S, u = set / S, c = set % C::SLOTS, cu = set / C::SLOTS;
+        uint32_t dst = stage0 + (uint32_t)(s * C::STAGE) + at + (uint32_t)(swz << 4);
+        uint32_t src = codes + (uint32_t)(c * C::SLOT);
+        int win_in = -1;  // FWD: the last window waited for
+        for (int j = set; j < total; j += SETS) {
+          const int i = s_lo + li, k = column();
+          uint32_t w[2][B];
+          uint16_t sv[2], zv[2];
+          wait_fast(cfull0 + 8 * c, cu & 1, abort_flag);
+          read_codes<B>(src, OP == FWD ? (B == 3 ? (i & 1) * 24 : 0) : (blk & 1) * 8 * B, cswz, w);
+          if (p.sb_tma) {
+            uint32_t o = sbs + ((k >> p.lgs) & 7) * 2;
+            if constexpr (OP == FWD) {
+              const int win = lt * nwin + (i >> spw) - (s_lo >> spw);
+              if (win != win_in) wait_fast(wfull0 + 8 * (win & 1), (win >> 1) & 1, abort_flag);
+              win_in = win;
+              o += (uint32_t)((win & 1) * C::WINDOW);
+            } else {
+              o += (uint32_t)(c * C::SLOT);
+            }
+            sv[0] = sv[1] = lds_u16(o);
+            zv[0] = zv[1] = lds_u16(o + C::SB);
+            if (p.lgs == 5) {  // 64 codes are two groups
+              sv[1] = lds_u16(o + 2);
+              zv[1] = lds_u16(o + C::SB + 2);
+            }
+          } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) sv[h] = sn[h], zv[h] = zn[h];
-        }
-        li += SETS;
-        if (li >= nk) settle();
-        if (!p.sb_tma) fetch(sn, zn);
-        // all of the unit before the wait for its stage, which the MMAs of S steps
-        // ago hold: what then stands between them and the next is the store alone
-        uint4 v[8];
+            for (int h = 0; h < 2; ++h) sv[h] = sn[h], zv[h] = zn[h];
+          }
+          li += SETS;
+          if (li >= nk) settle();
+          if (!p.sb_tma) fetch(sn, zn);
+          // all of the unit before the wait for its stage, which the MMAs of S steps
+          // ago hold: what then stands between them and the next is the store alone
+          uint4 v[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          v[q] = dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3);
-          asm volatile("" ::"r"(v[q].x), "r"(v[q].y), "r"(v[q].z), "r"(v[q].w));
-        }
-        if (u > 0) wait_fast(empty0 + 8 * s, (u - 1) & 1, abort_flag);
+          for (int q = 0; q < 8; ++q) {
+            v[q] = dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3);
+            asm volatile("" ::"r"(v[q].x), "r"(v[q].y), "r"(v[q].z), "r"(v[q].w));
+          }
+          if (u > 0) wait_fast(empty0 + 8 * s, (u - 1) & 1, abort_flag);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sts_v4(dst ^ (uint32_t)(q << 4), v[q]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (PAIR)
-            arrive_remote(lfull0 + 8 * s);
-          else
-            mbar_arrive(full0 + 8 * s);
-          mbar_arrive(cempty0 + 8 * c);
+          for (int q = 0; q < 8; ++q) sts_v4(dst ^ (uint32_t)(q << 4), v[q]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR)
+              arrive_remote(lfull0 + 8 * s);
+            else
+              mbar_arrive(full0 + 8 * s);
+            mbar_arrive(cempty0 + 8 * c);
+          }
+          s += SETS, dst += SETS * C::STAGE;
+          if (s >= S) s -= S, ++u, dst -= S * C::STAGE;
+          c += SETS, src += SETS * C::SLOT;
+          if (c >= C::SLOTS) c -= C::SLOTS, ++cu, src -= C::SLOTS * C::SLOT;
         }
-        s += SETS, dst += SETS * C::STAGE;
-        if (s >= S) s -= S, ++u, dst -= S * C::STAGE;
-        c += SETS, src += SETS * C::SLOT;
-        if (c >= C::SLOTS) c -= C::SLOTS, ++cu, src -= C::SLOTS * C::SLOT;
       }
     }
-   }
   }
 
   // ---------------- epilogue ----------------
@@ -1228,7 +1231,8 @@ cudaError_t launch(const Args& p, const Maps& tm, int clusters, cudaStream_t st)
   using C = Cfg<OP, B, PAIR>;
   static int configured[64] = {0};
   const int per = (PAIR ? 2 : 1) * p.splits;
-  return launch_kernel(pair_gemm_kernel<OP, B, T, PAIR>, configured, clusters * per, C::THREADS, C::SMEM, per, st, p, tm);
+  return launch_kernel(pair_gemm_kernel<OP, B, T, PAIR>, configured, clusters * per, C::THREADS, C::SMEM, per, st, p,
+                       tm);
 }
 
 template <int OP, int B, bool PAIR>
@@ -1244,7 +1248,8 @@ cudaError_t dispatch(int op, bool pair, Args& p, Maps& tm, int clusters, cudaStr
   if (op == DP) return launch<DP, B, __nv_bfloat16, true>(p, tm, clusters, st);
   p.sb_tma = (p.K >> p.lgs) % 8 == 0;
   for (int i = 0; i < p.parts; ++i)
-    if (!(op == FWD ? make_code_maps<FWD, B>(&tm, i, p) : make_code_maps<DX, B>(&tm, i, p))) return cudaErrorNotSupported;
+    if (!(op == FWD ? make_code_maps<FWD, B>(&tm, i, p) : make_code_maps<DX, B>(&tm, i, p)))
+      return cudaErrorNotSupported;
   if (op == DX) return launch_t<DX, B, true>(p, tm, clusters, st);
   return pair ? launch_t<FWD, B, true>(p, tm, clusters, st) : launch_t<FWD, B, false>(p, tm, clusters, st);
 }
