@@ -432,6 +432,26 @@ __device__ __forceinline__ void store8(T* dst, const float* v, bool vec, int cnt
   }
 }
 
+// N values (2 or 4) at a multiple of N, in one store
+template <int N>
+__device__ __forceinline__ void store_run(void* base, int dtype, int64_t at, const float* v) {
+  if (dtype == QMM_F32) {
+    if constexpr (N == 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(base) + at) = make_float2(v[0], v[1]);
+    return;
+  }
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i)
+    w[i] = dtype == QMM_BF16 ? pack2<__nv_bfloat16>(v[2 * i], v[2 * i + 1]) : pack2<__half>(v[2 * i], v[2 * i + 1]);
+  if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + at) = w[0];
+}
+
 // SiLU(g) * u within 2^-19
 __device__ __forceinline__ float silu_mul(float g, float u) { return g * __fdividef(1.0f, 1.0f + __expf(-g)) * u; }
 
@@ -910,15 +930,15 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
       fence_after();
       const uint32_t acc = lanes + (uint32_t)(b * 256);
       if constexpr (OP == DP) {
-        // 128 columns of one weight row: units of 32, groups of 1, 2 or 4
-        const int lu = p.lgs - 5;  // log2 of the units per group
-        const int64_t G = p.K >> p.lgs;
+        // 128 columns of one weight row: sums of units of 32, then groups of 1, 2
+        // or 4 units, stored together where they are aligned
+        const int G = p.K >> p.lgs, k0 = tl.n0 + c0;
         const bool live = row < p.N;
-        float2 sq = make_float2(0.0f, 0.0f), sv = sq;
+        float ds[4], dz[4];
 #pragma unroll
         for (int un = 0; un < 4; ++un) {
-          const int k = tl.n0 + c0 + un * 32;
-          if (k < p.K) {
+          float2 sq = make_float2(0.0f, 0.0f), sv = sq;
+          if (k0 + un * 32 < p.K) {
             const uint32_t(&w)[B] = codes[un];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -934,20 +954,35 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                   const float2 x = make_float2(v[i], v[i + 1]);
-                  const float2 q = codes2<B>(w, hf * 16 + i);
-                  sq = fma2f(x, q, sq);
+                  sq = fma2f(x, codes2<B>(w, hf * 16 + i), sq);
                   sv = add2(sv, x);
                 }
               }
             }
-            if (((un + 1) & ((1 << lu) - 1)) == 0) {
-              if (live) {
-                const int64_t at = (int64_t)row * G + (k >> p.lgs);
-                store_as(p.out[2 * tl.part], p.out_dtype, at, sq.x + sq.y);
-                store_as(p.out[2 * tl.part + 1], p.out_dtype, at, sv.x + sv.y);
-              }
-              sq = sv = make_float2(0.0f, 0.0f);
-            }
+          }
+          ds[un] = sq.x + sq.y;
+          dz[un] = sv.x + sv.y;
+        }
+        if (live && k0 < p.K) {
+          if (p.lgs > 5) {
+            ds[0] += ds[1], ds[1] = ds[2] + ds[3];
+            dz[0] += dz[1], dz[1] = dz[2] + dz[3];
+          }
+          if (p.lgs > 6) ds[0] += ds[1], dz[0] += dz[1];
+          const int64_t at = (int64_t)row * G + (k0 >> p.lgs);
+          const int n = min(128, p.K - k0) >> p.lgs;  // groups
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            void* dst = p.out[2 * tl.part + o];
+            const float* v = o ? dz : ds;
+            if (n == 4 && G % 4 == 0)
+              store_run<4>(dst, p.out_dtype, at, v);
+            else if (n == 2 && G % 2 == 0)
+              store_run<2>(dst, p.out_dtype, at, v);
+            else
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (i < n) store_as(dst, p.out_dtype, at + i, v[i]);
           }
         }
       } else if (splits > 1) {
