@@ -911,15 +911,24 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
       const Tile tl = tile_of<OP, PAIR>(p, cluster + lt * clusters);
       const int b = lt & 1;
       const int row = tl.m0 + 128 * side + r;
-      // DP: the codes of the lane's row, requested while the products run
+      // DP: the codes of the lane's row, requested while the products run: 128
+      // codes are 16 B bytes, in 16-byte loads where rows start on 16 bytes
       uint32_t codes[4][B ? B : 1];
       const int c0 = OP == DP ? (((warp - 2) >> 2) & 1) * 128 : 0;
       if constexpr (OP == DP) {
+        const int k0 = tl.n0 + c0;
+        const uint32_t* src = p.w[tl.part].packed + ((int64_t)row * (p.K >> 5) + (k0 >> 5)) * B;
+        if (row < p.N && (p.K >> 5) * B % 4 == 0 && k0 + 128 <= p.K) {
+          uint32_t* flat = &codes[0][0];
 #pragma unroll
-        for (int un = 0; un < 4; ++un) {
-          const int k = tl.n0 + c0 + un * 32;
-          if (row < p.N && k < p.K)
-            load_words<B>(p.w[tl.part].packed + ((int64_t)row * (p.K >> 5) + (k >> 5)) * B, codes[un]);
+          for (int i = 0; i < B; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            flat[4 * i] = v.x; flat[4 * i + 1] = v.y; flat[4 * i + 2] = v.z; flat[4 * i + 3] = v.w;
+          }
+        } else if (row < p.N) {
+#pragma unroll
+          for (int un = 0; un < 4; ++un)
+            if (k0 + un * 32 < p.K) load_words<B>(src + un * B, codes[un]);
         }
       }
       if (!failed) {
