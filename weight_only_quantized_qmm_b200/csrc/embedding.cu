@@ -146,8 +146,7 @@ __global__ void __launch_bounds__(kLookThreads) lookup_kernel(const LookArgs p) 
 constexpr int kSortThreads = 512, kSortWarps = 16;  // of each sorting CTA
 constexpr int kHeld = 4;            // list entries a lane keeps between a pass's two readings
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
-constexpr int kSlabThreads = 128;   // 8 columns each
-constexpr int kSlab = kSlabThreads * 8;
+constexpr int kSlabThreads = 128;   // most of a block of sums, 16 columns each
 
 struct SortArgs {
   const int32_t* ids;
@@ -318,7 +317,7 @@ struct GradArgs {
   float* part;  // [chunk][first run | last run][scales | biases][groups]
 };
 
-// P list entries x 1024 columns a block; 8 columns a thread.
+// P list entries x up to 2048 columns a block; 16 columns a thread.
 template <int B, typename TD>
 __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -329,30 +328,30 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
   const uint32_t key = lane < cnt ? p.keys[e0 + lane] : 0xffffffffu;
   const uint32_t tok = lane < cnt ? p.perm[e0 + lane] : 0u;
   const uint32_t prev = e0 > 0 ? p.keys[e0 - 1] : 0xffffffffu, next = e0 + cnt < p.n ? p.keys[e0 + cnt] : 0xffffffffu;
-  const int col = blockIdx.y * kSlab + threadIdx.x * 8;
+  const int col = (blockIdx.y * blockDim.x + threadIdx.x) * 16;
   const bool live = col < p.cols;  // (threads past the row read its start and store nothing)
   const uint8_t* dy = reinterpret_cast<const uint8_t*>(p.dy) + (live ? col : 0) * (int)sizeof(TD);
   const uint32_t dy_row = (uint32_t)p.cols * (uint32_t)sizeof(TD), code_row = (uint32_t)(p.cols >> 3) * B;
   const uint8_t* codes = reinterpret_cast<const uint8_t*>(p.packed) + (int64_t)(col >> 3) * B;
   const int G = p.cols >> p.lgs, g = col >> p.lgs;
-  const int lpg = 1 << (p.lgs - 3);  // threads of a group
+  const int lpg = 1 << (p.lgs - 4);  // threads of a group
   // after the group's sum, its first thread holds the scale's, its second the bias's
   const bool odd = threadIdx.x & 1, stores = live && (threadIdx.x & (lpg - 1)) < 2;
   const uint32_t out_row = (uint32_t)G * (p.g_dtype == QMM_F32 ? 4u : 2u);
   uint8_t* const out =
       reinterpret_cast<uint8_t*>(odd ? p.out[1] : p.out[0]) + (int64_t)g * (p.g_dtype == QMM_F32 ? 4 : 2);
-  constexpr int U = sizeof(TD) == 4 ? 4 : 8;  // rows requested at a time
+  constexpr int U = sizeof(TD) == 4 ? 2 : 4;  // rows requested at a time
   const uint32_t after = __shfl_down_sync(0xffffffffu, key, 1);
   // the entries after which a run or the chunk ends
   const uint32_t ends = __ballot_sync(0xffffffffu, lane < cnt && (lane + 1 == cnt || after != key));
-  float2 acc[4];
+  float2 acc[8];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.0f, 0.0f);
+  for (int c = 0; c < 8; ++c) acc[c] = make_float2(0.0f, 0.0f);
   int start = 0;
   for (int i0 = 0; i0 < cnt; i0 += U) {
     // U rows of dy, and the codes of the rows whose runs end among them
-    uint4 raw[U][sizeof(TD) / 2];
-    uint32_t code[U][3];
+    uint4 raw[U][sizeof(TD)];
+    uint32_t code[U][2][3];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       // (lanes past the chunk hold token 0: a valid row, and what a bad id's
@@ -360,37 +359,38 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
       const uint32_t t = __shfl_sync(0xffffffffu, tok, (i0 + j) & 31);
       const uint4* src = reinterpret_cast<const uint4*>(dy + (uint64_t)t * dy_row);
 #pragma unroll
-      for (int h = 0; h < (int)sizeof(TD) / 2; ++h) raw[j][h] = __ldcs(src + h);
+      for (int h = 0; h < (int)sizeof(TD); ++h) raw[j][h] = __ldcs(src + h);
       if (ends >> ((i0 + j) & 31) & 1u) {
         const uint32_t k = __shfl_sync(0xffffffffu, key, (i0 + j) & 31);
-        if (live && k < (uint32_t)p.rows)
-          load8<B>(codes + (uint64_t)k * code_row, code[j]);
+        if (live && k < (uint32_t)p.rows) {
+          load8<B>(codes + (uint64_t)k * code_row, code[j][0]);
+          load8<B>(codes + (uint64_t)k * code_row + B, code[j][1]);
+        }
       }
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int i = i0 + j;
       if (i >= cnt) break;
-      __align__(16) TD v[8];
+      __align__(16) TD v[16];
       memcpy(v, raw[j], sizeof(v));
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = add2(acc[c], make_float2(to_f32(v[2 * c]), to_f32(v[2 * c + 1])));
+      for (int c = 0; c < 8; ++c) acc[c] = add2(acc[c], make_float2(to_f32(v[2 * c]), to_f32(v[2 * c + 1])));
       if (!(ends >> i & 1u)) continue;  // the run goes on
       const uint32_t k = __shfl_sync(0xffffffffu, key, i);
       if (k < (uint32_t)p.rows) {
         float2 s2 = make_float2(0.0f, 0.0f), b2 = s2;
         if (live) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            s2 = fma2f(acc[c], codes2<B>(code[j], 2 * c), s2);
+          for (int c = 0; c < 8; ++c) {
+            s2 = fma2f(acc[c], codes2<B>(code[j][c >> 2], 2 * (c & 3)), s2);
             b2 = add2(b2, acc[c]);
           }
         }
         const float ds = s2.x + s2.y, db = b2.x + b2.y;
         float v = (odd ? db : ds) + __shfl_xor_sync(0xffffffffu, odd ? ds : db, 1);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        if (lpg > 2) v += __shfl_xor_sync(0xffffffffu, v, 2);
         if (lpg > 4) v += __shfl_xor_sync(0xffffffffu, v, 4);
-        if (lpg > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
         if (stores) {
           if ((start == 0 && prev == k) || (i + 1 == cnt && next == k))  // a piece of a longer run
             p.part[(((int64_t)chunk * 2 + (start == 0 ? 0 : 1)) * 2 + odd) * G + g] = v;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kSlabThreads) grad_kernel(const GradArgs p) {
         }
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.0f, 0.0f);
+      for (int c = 0; c < 8; ++c) acc[c] = make_float2(0.0f, 0.0f);
       start = i + 1;
     }
   }
@@ -578,9 +578,12 @@ __global__ void __launch_bounds__(kShortThreads, kShortBlocks) short_kernel(cons
   }
 }
 
+// Threads of a block of sums: whole warps over the columns, up to kSlabThreads.
+static int slab_threads(int64_t cols) { return (int)std::min<int64_t>(kSlabThreads, (cols + 511) / 512 * 32); }
+
 // Tokens of a chunk: up to 32 (one a lane), fewer while that leaves SMs idle.
 static int chunk_of(int64_t n, int64_t cols) {
-  const int64_t slabs = (cols + kSlab - 1) / kSlab;
+  const int64_t slabs = (cols + 16 * slab_threads(cols) - 1) / (16 * slab_threads(cols));
   int c = 32;
   while (c > 4 && (n + c - 1) / c * slabs < 4 * 148) c /= 2;
   return c;
@@ -691,13 +694,14 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
   ga.out[1] = dbiases;
   ga.g_dtype = g_dtype;
   ga.part = reinterpret_cast<float*>(ws + 4 * n4);
-  const dim3 grid(ga.chunks, (unsigned)((w->cols + kSlab - 1) / kSlab));
+  const int threads = slab_threads(w->cols);
+  const dim3 grid(ga.chunks, (unsigned)((w->cols + 16 * threads - 1) / (16 * threads)));
   switch (w->bits) {
-    case 2: e = launch_next(grad_kernel<2, TD>, grid, kSlabThreads, 1, ga, st); break;
-    case 3: e = launch_next(grad_kernel<3, TD>, grid, kSlabThreads, 1, ga, st); break;
-    case 4: e = launch_next(grad_kernel<4, TD>, grid, kSlabThreads, 1, ga, st); break;
-    case 6: e = launch_next(grad_kernel<6, TD>, grid, kSlabThreads, 1, ga, st); break;
-    default: e = launch_next(grad_kernel<8, TD>, grid, kSlabThreads, 1, ga, st); break;
+    case 2: e = launch_next(grad_kernel<2, TD>, grid, threads, 1, ga, st); break;
+    case 3: e = launch_next(grad_kernel<3, TD>, grid, threads, 1, ga, st); break;
+    case 4: e = launch_next(grad_kernel<4, TD>, grid, threads, 1, ga, st); break;
+    case 6: e = launch_next(grad_kernel<6, TD>, grid, threads, 1, ga, st); break;
+    default: e = launch_next(grad_kernel<8, TD>, grid, threads, 1, ga, st); break;
   }
   if (e != cudaSuccess || ga.chunks == 1) return e;
   return launch_next(join_kernel, dim3(ga.chunks - 1), 128, 1, ga, st);
