@@ -431,8 +431,8 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
 qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, float alpha, void* out,
                          qmm_dtype out_dtype, int32_t* d_status, void* stream);
 
-/* Workspace bytes of qmm_embedding_backward (-1 when n is outside [0, 2^30],
- * rows outside [0, 2^31 - 2] or cols outside [1, 2^25]). */
+/* Workspace bytes of qmm_embedding_backward (-1 when n or rows is outside
+ * [0, 2^30] or cols outside [1, 2^25]). */
 int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
 
 /* Gradient of the lookup in the table's scales and biases, with
@@ -444,14 +444,14 @@ int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t 
  * outside [0, w->rows) adds nothing and sets QMM_ERR_BAD_TOKEN_ID in *d_status
  * (may be NULL).
  * Errors: qmm_dequantize's for w; UNSUPPORTED (microscaled, device), DTYPE,
- * INVALID_ARG (n, workspace_bytes), ALIGNMENT (dy, dscales, dbiases, workspace
+ * INVALID_ARG (n, rows, cols, workspace_bytes), ALIGNMENT (dy, dscales, dbiases, workspace
  * 16-byte, ids and d_status 4-byte), CUDA. */
 qmm_status qmm_embedding_backward(const void* dy, qmm_dtype dy_dtype, const int32_t* ids, int64_t n,
                                   const qmm_qweight* w, float alpha, void* dscales, void* dbiases,
                                   qmm_dtype g_dtype, void* workspace, int64_t workspace_bytes, int32_t* d_status,
                                   void* stream);
 
-/* Workspace bytes of qmm_gate_up_silu (-1 for a size outside [0, 2^31 - 1],
+/* Workspace bytes of qmm_gate_up_silu (-1 for a size outside [0, 2^31 - 1024],
  * M * F or F * K past 2^57, or a K that cannot be packed in `bits`): room for
  * both dequantized weights for many tokens and for rows of codes that do not
  * start on 16 bytes, 0 otherwise. */
@@ -464,13 +464,13 @@ int64_t qmm_gate_up_silu_workspace_bytes(int64_t M, int64_t K, int64_t F, int bi
  * (both NULL, or both [M, F] in x_dtype) receive the two projections, which
  * the backward pass reads.  M == 0 or F == 0 is a no-op.
  * Errors: INVALID_ARG (shape rules, K, gate and up differ, one of g_pre and
- * u_pre missing, workspace_bytes), UNSUPPORTED (see above, sizes past 2^31 - 1,
+ * u_pre missing, workspace_bytes), UNSUPPORTED (see above, sizes past 2^31 - 1024,
  * device), DTYPE, ALIGNMENT (x, h, g_pre, u_pre, workspace 16-byte), CUDA. */
 qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,
                             const qmm_qweight* up, void* h, qmm_dtype h_dtype, void* g_pre, void* u_pre,
                             void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1],
+/* Workspace bytes of qmm_matmul_backward (-1 for a size outside [0, 2^31 - 1024],
  * M * N or N * K past 2^57, or a K that cannot be packed in `bits`). */
 int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits);
 
@@ -486,7 +486,7 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of qmm_gate_up_silu_backward (-1 for a size outside
- * [0, 2^31 - 1], M * F or F * K past 2^57, or a K that cannot be packed in
+ * [0, 2^31 - 1024], M * F or F * K past 2^57, or a K that cannot be packed in
  * `bits`). */
 int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits);
 

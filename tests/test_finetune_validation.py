@@ -149,3 +149,28 @@ def test_binding():
     small = host()
     small.scales = small.scales[:31]
     refuses("gate: qmm: scales holds", lambda: api.qmm_gate_up_silu(x, small, w))
+
+
+def test_largest_sizes(L):
+    """Rows and columns past the last one of a tile are counted in 32 bits too."""
+    most = 2 ** 31 - 1024
+    for need in (L.qmm_matmul_backward_workspace_bytes, L.qmm_gate_up_silu_backward_workspace_bytes,
+                 L.qmm_gate_up_silu_workspace_bytes):
+        assert need(most, 32, 8, 4) >= 0 and need(8, most, 8, 4) >= 0 and need(8, 32, most, 4) >= 0
+        assert need(most + 1, 32, 8, 4) == need(8, most + 32, 8, 4) == need(8, 32, most + 1, 4) == -1
+
+    def gate_up(M, rows):
+        g = u = qw(rows=rows)
+        return L.qmm_gate_up_silu(A, BF, M, 128, ctypes.byref(g), ctypes.byref(u), A, BF, None, None, A, 1 << 60, None)
+
+    def matmul(M, rows):
+        w = qw(rows=rows)
+        return L.qmm_matmul_backward(A, A, BF, M, 128, ctypes.byref(w), A, A, A, BF, A, 1 << 60, None)
+
+    for call in (gate_up, matmul):
+        assert call(most + 1, 8) == call(2 ** 31 - 1, 8) == call(20, most + 1) == _lib.QMM_ERR_UNSUPPORTED
+    need = L.qmm_embedding_backward_workspace_bytes
+    assert need(10, 2 ** 30, 32) >= 0 and need(10, 2 ** 30 + 1, 32) == need(10, 2 ** 31 - 2, 32) == -1
+    w = qw(rows=2 ** 31 - 2)
+    assert L.qmm_embedding_backward(A, BF, A, 10, ctypes.byref(w), 1.0, A, A, BF, A, 1 << 60, None,
+                                    None) == _lib.QMM_ERR_INVALID_ARG

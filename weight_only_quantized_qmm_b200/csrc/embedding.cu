@@ -730,9 +730,8 @@ qmm_status qmm_embedding(const int32_t* ids, int64_t n, const qmm_qweight* w, fl
 }
 
 int64_t qmm_embedding_backward_workspace_bytes(int64_t n, int64_t rows, int64_t cols) {
-  if (n < 0 || n > (1 << 30) || rows < 0 || rows >= (int64_t)INT32_MAX || cols <= 0 ||
-      cols > (1 << 25))
-    return -1;
+  // (rows and list entries past the last one of a block's share are counted in 32 bits)
+  if (n < 0 || n > (1 << 30) || rows < 0 || rows > (1 << 30) || cols <= 0 || cols > (1 << 25)) return -1;
   return qmm::embed::grad_workspace(n, cols);
 }
 

@@ -287,7 +287,8 @@ namespace {
 
 constexpr int64_t kFewTokens = 16;  // tokens of the streaming kernels
 
-bool i32(int64_t v) { return v >= 0 && v <= (int64_t)INT32_MAX; }
+// sizes: 32 bits, and so are the rows and columns past the last one of a tile
+bool i32(int64_t v) { return v >= 0 && v <= (int64_t)INT32_MAX - 1023; }
 // M rows of n elements (padded) and n rows of K, all within 2^57 elements
 bool fits(int64_t M, int64_t K, int64_t n) {
   return std::max(M, K) <= ((int64_t)1 << 57) / (n + 8);
@@ -350,7 +351,7 @@ qmm_status qmm_gate_up_silu(const void* x, qmm_dtype x_dtype, int64_t M, int64_t
 int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int bits) {
   if (!i32(M) || !i32(K) || !i32(N) || !fits(M, K, N) || qmm_packed_words_per_row(K, bits) < 0) return -1;
   // rows of dy that do not start on 16 bytes are copied to ones that do
-  return qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) + 
+  return qmm::ffn::align16(N % 8 ? M * qmm::ffn::padded(N) * 2 : 0) +
          qmm::ffn::dense_bytes(qmm::pg::DX, M, K, N, bits, 1);
 }
 
@@ -385,7 +386,7 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
 
 int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t F, int bits) {
   if (!i32(M) || !i32(K) || !i32(F) || !fits(M, K, F) || qmm_packed_words_per_row(K, bits) < 0) return -1;
-  return qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) + 
+  return qmm::ffn::align16(2 * M * qmm::ffn::padded(F) * 2) +
          qmm::ffn::dense_bytes(qmm::pg::DX, M, K, F, bits, 2);  // dg and du first
 }
 
