@@ -42,9 +42,9 @@ __global__ void __launch_bounds__(256)
 act_grad_kernel(const T* __restrict__ dh, const T* __restrict__ g, const T* __restrict__ u, int64_t n, int F, int ld,
                 T* __restrict__ dg, T* __restrict__ du) {
   auto grad = [](float a, float b, float c, float& x, float& y) {
-    const float p = __fdividef(1.0f, 1.0f + __expf(-b));  // within 2^-19; the results are rounded to 16 bits
-    x = a * c * (p * (1.0f + b * (1.0f - p)));
-    y = a * (b * p);
+    const float2 p = pg::logistic<T>(b);
+    x = a * c * (p.x * fmaf(b, p.y, 1.0f));
+    y = a * (b * p.x);
   };
   const int64_t step = (int64_t)gridDim.x * blockDim.x, first = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   if constexpr (VEC) {
