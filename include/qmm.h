@@ -478,7 +478,8 @@ int64_t qmm_matmul_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int
  * dequant(W) in x_dtype, and dscales, dbiases [N, K / group_size] in g_dtype
  * (x_dtype or QMM_F32) with dW = dy^T x.  dy: [M, N], x: [M, K] in x_dtype.  dx
  * may be NULL, or both dscales and dbiases (x is then not read).  M == 0
- * writes zero parameter gradients, N == 0 a zero dx.
+ * writes zero parameter gradients, N == 0 a zero dx; M == 0 without parameter
+ * gradients, or N == 0 without dx, is a no-op.
  * Errors: INVALID_ARG (shape rules, K, nothing to compute, workspace_bytes),
  * UNSUPPORTED, DTYPE, ALIGNMENT (16-byte), CUDA. */
 qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype, int64_t M, int64_t K,
@@ -496,7 +497,8 @@ int64_t qmm_gate_up_silu_backward_workspace_bytes(int64_t M, int64_t K, int64_t 
  *   dgate_scales, dgate_biases from dW = dg^T x, dup_scales, dup_biases from
  *   dW = du^T x, [F, K / group_size] each in g_dtype (x_dtype or QMM_F32).
  * dh, g_pre, u_pre: [M, F] in x_dtype.  dx may be NULL, or all four parameter
- * gradients.  M == 0 writes zero parameter gradients, F == 0 a zero dx.
+ * gradients.  M == 0 writes zero parameter gradients, F == 0 a zero dx; M == 0
+ * without parameter gradients, or F == 0 without dx, is a no-op.
  * Errors: as qmm_matmul_backward and qmm_gate_up_silu. */
 qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* g_pre, const void* u_pre,
                                      qmm_dtype x_dtype, int64_t M, int64_t K, const qmm_qweight* gate,

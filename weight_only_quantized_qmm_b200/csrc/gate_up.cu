@@ -316,6 +316,13 @@ qmm_status check_pair(const qmm_qweight* gate, const qmm_qweight* up, qmm_dtype 
                                                                                                 : QMM_ERR_INVALID_ARG;
 }
 
+// A gradient call whose every output is not asked for or holds no elements: the
+// dx of no tokens, the parameter gradients of no rows (an empty tensor's address
+// may be null, as that of an output that is not asked for is).
+bool nothing_to_write(int64_t M, int64_t rows, const void* dx, const void* grad) {
+  return (M == 0 && !grad) || (rows == 0 && !dx);
+}
+
 }  // namespace
 
 extern "C" {
@@ -361,7 +368,9 @@ qmm_status qmm_matmul_backward(const void* dy, const void* x, qmm_dtype x_dtype,
   qmm_status s = check_weight(w, x_dtype, M, K);
   if (s != QMM_OK) return s;
   if (!dtype_ok(g_dtype) || (g_dtype != x_dtype && g_dtype != QMM_F32)) return QMM_ERR_DTYPE;
-  if ((dscales == nullptr) != (dbiases == nullptr) || (!dx && !dscales)) return QMM_ERR_INVALID_ARG;
+  if ((dscales == nullptr) != (dbiases == nullptr)) return QMM_ERR_INVALID_ARG;
+  if (nothing_to_write(M, w->rows, dx, dscales)) return QMM_OK;
+  if (!dx && !dscales) return QMM_ERR_INVALID_ARG;
   const int64_t need = qmm_matmul_backward_workspace_bytes(M, K, w->rows, w->bits);
   if (need < 0 || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
   if (M > 0 && w->rows > 0 && (!aligned16(dy) || (dscales && !aligned16(x)))) return QMM_ERR_ALIGNMENT;
@@ -401,6 +410,7 @@ qmm_status qmm_gate_up_silu_backward(const void* dh, const void* x, const void* 
   void* const grads[4] = {dgate_scales, dgate_biases, dup_scales, dup_biases};
   for (int i = 1; i < 4; ++i)
     if ((grads[i] == nullptr) != (grads[0] == nullptr)) return QMM_ERR_INVALID_ARG;
+  if (nothing_to_write(M, gate->rows, dx, grads[0])) return QMM_OK;
   if (!dx && !grads[0]) return QMM_ERR_INVALID_ARG;
   const int64_t F = gate->rows;
   const int64_t need = qmm_gate_up_silu_backward_workspace_bytes(M, K, F, gate->bits);
