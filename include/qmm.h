@@ -410,7 +410,9 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
  * weight is rounded once to it (as in qmm_matmul), and so are dg and du of
  * the gated block's gradient.  An f32 output is the same arithmetic without
  * the last rounding.  Results do not depend on timing: the same call gives
- * the same bits.
+ * the same bits.  These calls take no status buffer: a device-side timeout
+ * writes the affected tiles as NaN, and leaves the gated projection of up to 16
+ * tokens incomplete.
  *
  * No output overlaps an input, a workspace or another output.
  *

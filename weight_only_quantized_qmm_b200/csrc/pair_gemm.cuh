@@ -35,7 +35,8 @@
 // of the leader CTA); 2.. epilogue (4 warps; DP two sets of 8, one for
 // each accumulator); then the producer of the
 // codes and the 16 dequant warps.
-// Every wait is bounded; after one that gave up the tiles are written as NaN.
+// Every wait is bounded; after one that gave up both CTAs of a pair write their
+// tiles as NaN (after one of an epilogue, that CTA its rows).
 #pragma once
 
 #include <cuda.h>
@@ -192,13 +193,27 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, cons
   }
   return false;
 }
+// Raises the abort flag, PAIR: of both CTAs.  The operands that one of them fails
+// to deliver enter the accumulators of both, and after a failure of the issuer the
+// other CTA's epilogue is signalled too: each must know before it reads its half.
+template <bool PAIR>
+static __device__ __noinline__ void give_up(int* abort_flag) {
+  *reinterpret_cast<volatile int*>(abort_flag) = 1;
+  if constexpr (PAIR) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(su32(abort_flag), cta_rank() ^ 1u)), "r"(1u)
+                 : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
+}
 // One poll is the usual case; the full bounded wait stands aside, and one that
 // gives up raises the abort flag.
+template <bool PAIR>
 static __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, int* abort_flag) {
-  if (!wait(bar, parity, abort_flag)) *abort_flag = 1;
+  if (!wait(bar, parity, abort_flag)) give_up<PAIR>(abort_flag);
 }
+template <bool PAIR>
 __device__ __forceinline__ void wait_fast(uint32_t bar, uint32_t parity, int* abort_flag) {
-  if (!poll(bar, parity)) wait_slow(bar, parity, abort_flag);
+  if (!poll(bar, parity)) wait_slow<PAIR>(bar, parity, abort_flag);
 }
 template <bool PAIR>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar) {
@@ -642,7 +657,7 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
         const int row = tl.m0 + 128 * side;
         for (int i = s_lo; i < s_hi; ++i) {
           if (u > 0 && !wait(empty0 + 8 * s, (u - 1) & 1, abort_flag)) {
-            *abort_flag = 1;
+            give_up<PAIR>(abort_flag);
             stop = true;
             break;
           }
@@ -702,14 +717,14 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
       for (int lt = 0; lt < my_tiles && !stop; ++lt) {
         const int b = lt & 1;
         if (lt >= 2 && !wait_cluster(tfree0 + 8 * b, ((lt >> 1) - 1) & 1, abort_flag)) {
-          *abort_flag = 1;
+          give_up<PAIR>(abort_flag);
           break;
         }
         fence_after();
         const uint32_t acc = tmem + (uint32_t)(b * 256);
         for (int i = 0; i < nk; ++i) {
           if (!wait_cluster(full0 + 8 * s, u & 1, abort_flag)) {
-            *abort_flag = 1;
+            give_up<PAIR>(abort_flag);
             stop = true;
             break;
           }
@@ -791,7 +806,7 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
           }
           if (stop) {
             // (as the other producer: copies may be landing)
-            *abort_flag = 1;
+            give_up<PAIR>(abort_flag);
             for (int q = max(0, j - C::SLOTS); q < j; ++q)
               mbar_wait_n(cfull0 + 8 * (q % C::SLOTS), (q / C::SLOTS) & 1, 1u << 12);
             for (int q = max(0, win - 2); q < win; ++q) mbar_wait_n(wfull0 + 8 * (q & 1), (q >> 1) & 1, 1u << 12);
@@ -862,13 +877,13 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
           const int i = s_lo + li, k = column();
           uint32_t w[2][B];
           uint16_t sv[2], zv[2];
-          wait_fast(cfull0 + 8 * c, cu & 1, abort_flag);
+          wait_fast<PAIR>(cfull0 + 8 * c, cu & 1, abort_flag);
           read_codes<B>(src, OP == FWD ? (B == 3 ? (i & 1) * 24 : 0) : (blk & 1) * 8 * B, cswz, w);
           if (p.sb_tma) {
             uint32_t o = sbs + ((k >> p.lgs) & 7) * 2;
             if constexpr (OP == FWD) {
               const int win = lt * nwin + (i >> spw) - (s_lo >> spw);
-              if (win != win_in) wait_fast(wfull0 + 8 * (win & 1), (win >> 1) & 1, abort_flag);
+              if (win != win_in) wait_fast<PAIR>(wfull0 + 8 * (win & 1), (win >> 1) & 1, abort_flag);
               win_in = win;
               o += (uint32_t)((win & 1) * C::WINDOW);
             } else {
@@ -895,7 +910,7 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
             v[q] = dequant8<B, T>(w[q >> 2], sv[q >> 2], zv[q >> 2], q & 3);
             asm volatile("" ::"r"(v[q].x), "r"(v[q].y), "r"(v[q].z), "r"(v[q].w));
           }
-          if (u > 0) wait_fast(empty0 + 8 * s, (u - 1) & 1, abort_flag);
+          if (u > 0) wait_fast<PAIR>(empty0 + 8 * s, (u - 1) & 1, abort_flag);
 #pragma unroll
           for (int q = 0; q < 8; ++q) sts_v4(dst ^ (uint32_t)(q << 4), v[q]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
