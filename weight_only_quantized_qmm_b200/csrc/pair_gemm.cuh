@@ -817,6 +817,7 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
         // the sets of warps that fill a stage (PAIR: 128 rows of B, 4 warps;
         // single: 256, 8 warps) take turns
         constexpr int WPS = PAIR ? 4 : 8, SETS = kDeqWarps / WPS;
+        static_assert(C::SLOTS >= SETS && C::STAGES >= SETS, "one wrap a unit; older phases than the last are over");
         const int dw = warp - 3 - C::EPI, set = dw / WPS;
         const uint32_t lfull0 = PAIR ? map_rank(full0, lead) : full0;
         // this thread's 128 bytes of the operand tile: FWD, row r of B; DX, row
@@ -877,6 +878,13 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
           const int i = s_lo + li, k = column();
           uint32_t w[2][B];
           uint16_t sv[2], zv[2];
+          // Where a slot passes from set to set, this set has not seen its last codes
+          // land (copies may land out of order, and the parity of the phase before last
+          // would pass for this one's): those codes must be dequantized first.  That
+          // barrier cannot run ahead, since its next phase needs this set.
+          if constexpr (C::SLOTS % SETS != 0) {
+            if (cu > 0) wait_fast<PAIR>(cempty0 + 8 * c, (cu - 1) & 1, abort_flag);
+          }
           wait_fast<PAIR>(cfull0 + 8 * c, cu & 1, abort_flag);
           read_codes<B>(src, OP == FWD ? (B == 3 ? (i & 1) * 24 : 0) : (blk & 1) * 8 * B, cswz, w);
           if (p.sb_tma) {
