@@ -449,9 +449,13 @@ struct QgemvCfg {
   static constexpr int UG = UG0 < 1 ? 1 : UG0;                // groups per pipeline stage: 1, 2, 4 or 8
   static constexpr int SBW = UG == 1 ? 1 : UG / 2 + 1;        // scale (or bias) words per row per stage
   static constexpr int QW = NS * 2 * 2 * SBW;                 // scale+bias words per quad per stage
-  static constexpr int STAGES = 4;
   static constexpr int CODE_WORDS = UG * NS * 2 * SLOT * 32;  // per warp per stage
   static constexpr int STAGE_WORDS = CODE_WORDS + 8 * QW;     // + the 8 quads' scale/bias words
+  // four stages, or what fits 160 KB (gate and up of 6- or 8-bit codes in groups of
+  // 128: three or two), so that the partial sums and x fit beside the ring
+  static constexpr int FIT = 160 * 1024 / (kWarps * STAGE_WORDS * 4);
+  static constexpr int STAGES = FIT < 4 ? FIT : 4;
+  static_assert(STAGES >= 2, "a stage in flight while another is read");
   static constexpr int RING_BYTES = STAGES * STAGE_WORDS * 4; // per warp
   static constexpr int TOKP = MT * 8;
   static constexpr int CB = (UG + 7) / 8;                     // correction mmas per stage
