@@ -156,8 +156,8 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
 }
 // Bounded waits of this kernel: polls that may sleep up to kNap ns each (a
 // waiting warp that polls without a nap takes issue slots from the dequant
-// warps), giving up after kPolls of them or when another role has raised the
-// abort flag.
+// warps), giving up after kPolls of them (measured: 0.35 to 0.7 s) or when another
+// role has raised the abort flag.
 constexpr uint32_t kNap = 20000, kPolls = 1u << 17;
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -189,6 +189,17 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, cons
         : "r"(bar), "r"(parity), "r"(kNap)
         : "memory");
     if (done) return true;
+    if (*reinterpret_cast<const volatile int*>(abort_flag)) return false;
+  }
+  return false;
+}
+// Waits that last as long as whole sums (the epilogue's for a tile, in turn with
+// another's; the second CTA's for the last commit) get that bound for every 32768
+// steps of them, which take about 13 ms: 134 million tokens of a parameter gradient
+// are one tile of 0.7 s.
+__device__ __forceinline__ bool wait_steps(uint32_t bar, uint32_t parity, const int* abort_flag, int64_t steps) {
+  for (int64_t i = 0; i <= steps >> 15; ++i) {
+    if (wait(bar, parity, abort_flag)) return true;
     if (*reinterpret_cast<const volatile int*>(abort_flag)) return false;
   }
   return false;
@@ -704,7 +715,7 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
     // ---------------- MMA issuer ----------------
     if (PAIR && lane == 0 && !leader) {
       // (the leader's last commit arrives here too: nothing is on its way after it)
-      for (uint32_t i = 0; i < kPolls && !poll(drain, 0); ++i) {
+      for (int64_t i = 0; i < (int64_t)kPolls * (1 + ((int64_t)my_tiles * nk >> 15)) && !poll(drain, 0); ++i) {
       }
     } else if (lane == 0) {
       constexpr bool AMN = OP == DP, BMN = OP != FWD;
@@ -979,7 +990,7 @@ __device__ __forceinline__ void product(const Args& p, const Maps& tm, int block
         }
       }
       if (!failed) {
-        failed = !wait(accf0 + 8 * b, (lt >> 1) & 1, abort_flag) ||
+        failed = !wait_steps(accf0 + 8 * b, (lt >> 1) & 1, abort_flag, nk) ||
                  *reinterpret_cast<volatile int*>(abort_flag);
         failed = __any_sync(0xffffffffu, failed);
       }
