@@ -405,14 +405,15 @@ qmm_status qmm_moe_gemm_id_noalloc(const void* a, qmm_dtype a_dtype, const int32
  * The gated block and the matmul gradients take bf16 or f16 activations of
  * the scales' dtype, affine weights and the [N, K] layout (transpose = 1); f32
  * activations and the microscaled modes return QMM_ERR_UNSUPPORTED.  Their
- * products run on the tensor cores with fp32 accumulation.  For more than 16
- * tokens the operands are the activations' 16-bit type: each dequantized
- * weight is rounded once to it (as in qmm_matmul), and so are dg and du of
- * the gated block's gradient.  An f32 output is the same arithmetic without
- * the last rounding.  Results do not depend on timing: the same call gives
- * the same bits.  These calls take no status buffer: a device-side timeout
- * writes the affected tiles as NaN, and leaves the gated projection of up to 16
- * tokens incomplete.
+ * products run on the tensor cores with fp32 accumulation, which cuts what it
+ * adds: a sum of n terms is off by up to n / 16 * 2^-23 of their magnitudes' sum
+ * (4096 tokens: 2^-15).  For more than 16 tokens the operands are the
+ * activations' 16-bit type: each dequantized weight is rounded once to it (as in
+ * qmm_matmul), and so are dg and du of the gated block's gradient.  An f32 output
+ * leaves out the last rounding and takes the more accurate exponential.
+ * Results do not depend on timing: the same call gives the same bits.  These
+ * calls take no status buffer: a device-side timeout writes the affected tiles
+ * as NaN, and leaves the gated projection of up to 16 tokens incomplete.
  *
  * No output overlaps an input, a workspace or another output.
  *

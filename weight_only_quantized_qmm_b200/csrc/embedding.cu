@@ -581,7 +581,8 @@ __global__ void __launch_bounds__(kShortThreads, kShortBlocks) short_kernel(cons
 // Threads of a block of sums: whole warps over the columns, up to kSlabThreads.
 static int slab_threads(int64_t cols) { return (int)std::min<int64_t>(kSlabThreads, (cols + 511) / 512 * 32); }
 
-// Tokens of a chunk: up to 32 (one a lane), fewer while that leaves SMs idle.
+// Tokens of a chunk: up to 32 (one a lane), fewer while that leaves SMs idle.  (148
+// whatever the device: the workspace's size and the order of the sums follow it.)
 static int chunk_of(int64_t n, int64_t cols) {
   const int64_t slabs = (cols + 16 * slab_threads(cols) - 1) / (16 * slab_threads(cols));
   int c = 32;
@@ -674,7 +675,10 @@ static cudaError_t launch_grad(const void* dy, const int32_t* ids, int64_t n, co
   }
   sa.d_status = d_status;
   sa.zero_bytes = w->rows * G * qmm_host::dtype_size((qmm_dtype)g_dtype);
-  sa.ctas = n <= 2048 ? 1 : 8;  // (a cluster's barriers cost more than a short list's rounds)
+  // A cluster's barriers against a short list's rounds, us of the whole gradient with one
+  // CTA and with eight: rows of 4096 columns, 1024 tokens 14.4 and 17.3, 2048 20.7 and
+  // 20.5, 4096 34 and 28; rows of 1024 columns cross at 1000 (2048 tokens 16.6 and 13.6).
+  sa.ctas = n <= 2048 ? 1 : 8;
   const int ctas = qmm_host::num_sms() * 2 / sa.ctas * sa.ctas;
   cudaError_t e = launch_next(sort_kernel, dim3(ctas), kSortThreads, sa.ctas, sa, st);
   if (e != cudaSuccess) return e;

@@ -132,7 +132,10 @@ struct Plan {
 // dequantizing pass 2 us and its bytes at 4.5 TB/s.  Kernels that dequantize want
 // rows of codes on 16 bytes; dx runs on pairs only, which shares a launch with the
 // parameter gradients.  Clusters of 4 find room on 132 of the 148 SMs, clusters
-// of 8 on 120 (cudaOccupancyMaxActiveClusters).
+// of 8 on 120 (cudaOccupancyMaxActiveClusters).  Other widths are priced alike: at
+// each of them, 64 to 2048 tokens forward and dx, each way forced, the choice was
+// within 5% of the best, but for 2048 tokens of 8-bit bf16 codes, whose conversion
+// costs more (dx 222 us against 205 dense).
 static Plan plan_of(int op, int64_t M, int64_t K, int64_t N, int parts, int bits) {
   const int64_t out = op == pg::FWD ? N : K;  // columns of the output
   const int tn = op == pg::FWD ? 128 : 256;
@@ -285,7 +288,12 @@ using namespace qmm_host;
 
 namespace {
 
-constexpr int64_t kFewTokens = 16;  // tokens of the streaming kernels
+// Tokens of the streaming kernels, which keep the weights exact.  They are ahead of
+// the tensor cores up to 12 tokens (4096 x 14336 bf16, us: 9 tokens 34 against 62 at
+// 4 bits, 37 against 67 at 3; 12 tokens 37 against 59, 54 against 66 at 6) but for
+// 8-bit bf16 codes (74 against 69), and at 16 tokens for 2 and 3 bits (39 against 48,
+// 50 against 53); 4, 6 and 8 bits lose 13%, 8% and 24% there (48, 57, 81).
+constexpr int64_t kFewTokens = 16;
 
 // sizes: 32 bits, and so are the rows and columns past the last one of a tile
 bool i32(int64_t v) { return v >= 0 && v <= (int64_t)INT32_MAX - 1023; }
